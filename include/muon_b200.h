@@ -29,6 +29,10 @@
  *  - adamw_ema_batched: AdamW of the non-matrix tensors and the EMA of their
  *    new values in one pass (PR #1893, same table, row "Optimizer": AdamW on
  *    embeddings/scalars).
+ *  - adamw_mixed_batched: AdamW of many tensors with 32-bit or 8-bit moments,
+ *    fp32 or bf16 gradients, clipping by the global norm (grad_norm_batched)
+ *    and a bf16 copy of the new values; adam8_write_batched and
+ *    adam8_read_batched convert its 8-bit states.
  *
  * Conventions for every call:
  *  - Pointers named device point to device memory; pointers to structs and
@@ -224,6 +228,152 @@ muon_status_t adamw_ema_batched(const adamw_tensor_t *tensors, int32_t n_tensors
                                 const adamw_hyper_t *hyper, int32_t step,
                                 int32_t *step_dev, float ema_decay,
                                 muon_stream_t stream);
+
+/* ---- AdamW with 32-bit or 8-bit moments -----------------------------------
+ * The pages name AdamW on embeddings and scalars (PR #1893, table
+ * "Architecture and training stack", row "Optimizer") and print no state
+ * format; the calls below are this library's. */
+
+/* Element types of gradients and of plain moments. */
+typedef enum { MUON_F32 = 0, MUON_BF16 = 1 } muon_dtype_t;
+
+/* How 8-bit moments are rounded: to the nearest code (ties to even), or up
+ * with a probability equal to the place between the two codes (unbiased).
+ * Nearest leaves a second moment in place when a step moves it by less than
+ * half a code, which is so on most steps for beta2 of about 0.97 and more:
+ * take stochastic rounding there. */
+typedef enum { MUON_ROUND_NEAREST = 0, MUON_ROUND_STOCHASTIC = 1 } muon_round_t;
+
+/* Settings of adamw_mixed_batched.  lr, weight_decay, ema_decay finite;
+ * beta1, beta2 in [0, 1); eps >= 0.  seed gives the random bits of
+ * stochastic rounding, with the step number, the tensor's place in the call
+ * and the element's place in the tensor: the same call on the same inputs
+ * gives the same bits. */
+typedef struct {
+  double lr;
+  double beta1;
+  double beta2;
+  double eps;
+  double weight_decay;
+  double ema_decay;
+  uint64_t seed;
+  int32_t rounding; /* muon_round_t */
+} adamw_mixed_hyper_t;
+
+/* Elements that share one pair of scale bytes in an 8-bit state. */
+#define MUON_ADAM8_BLOCK 256
+
+/* One tensor of adamw_mixed_batched: device arrays of numel elements.
+ *  param       fp32, updated in place.
+ *  grad        fp32 or bf16 (grad_dtype), read only.
+ *  exp_avg, exp_avg_sq  the moments, updated in place: fp32 with scale NULL;
+ *              else one byte per element each, exp_avg_sq holding codes of
+ *              the second moment's root.
+ *  scale       NULL, or two bytes (first moment, root) for every 256
+ *              elements begun.  All bytes of the three arrays zero: moments
+ *              of zero, the state before the first step.
+ *  ema         fp32, updated in place, or NULL.
+ *  copy_bf16   receives the new parameters rounded to bf16, or NULL.
+ *  lr_scale, wd_scale  multiply lr and weight_decay for this tensor.
+ * fp32 arrays need 4-byte alignment, bf16 arrays 2-byte; tensors whose
+ * arrays are 16-byte aligned (codes: 8-byte) take the vectorised path.
+ * Arrays must not overlap, within a tensor or between tensors. */
+typedef struct {
+  float *param;
+  const void *grad;
+  void *exp_avg;
+  void *exp_avg_sq;
+  uint8_t *scale;
+  float *ema;
+  uint16_t *copy_bf16;
+  int64_t numel;
+  float lr_scale;
+  float wd_scale;
+  int32_t grad_dtype; /* muon_dtype_t */
+} adamw_mixed_tensor_t;
+
+/* AdamW step of every tensor, the EMA and the bf16 copy of the new
+ * parameters, in one pass; 32-bit and 8-bit states may be mixed in a call:
+ *   g  = c grad;  m' = b1 m + (1 - b1) g;  v' = b2 v + (1 - b2) g^2;
+ *   p' = p (1 - lr wd) - lr (m' / (1 - b1^t)) / (sqrt(v' / (1 - b2^t)) + eps);
+ *   e' = decay e + (1 - decay) p';  copy = bf16(p').
+ * The update uses m' and v' before they are rounded to 8 bits.
+ *  step, step_dev  t is `step` (>= 1) when step_dev is NULL; otherwise
+ *        step_dev points to two device int32: the steps taken so far (t is
+ *        one more; the call advances it) and a word for the call's own use,
+ *        zero before the first call.  One captured CUDA graph then serves
+ *        every step.  Calls that share a counter must be ordered.
+ *  lr_dev    NULL, or a device float read in place of hyper->lr.
+ *  coef_dev  NULL (c = 1), or a device float c, such as the second result of
+ *        grad_norm_batched.  If it is not finite the call changes nothing,
+ *        step_dev included.
+ * An 8-bit block in which a moment's magnitude is not finite or reaches 2^119
+ * reads as NaN from then on, all 256 elements.  A 32-bit second moment has
+ * fp32's range: c grad should lie between 1e-19 and 1e19, as far as it is
+ * not 0.  Up to 400 tensors per
+ * launch; at most 2^39 elements per call (MUON_ERR_UNSUPPORTED).
+ * Asynchronous on `stream`; argument errors are returned before anything is
+ * enqueued.  Deterministic. */
+muon_status_t adamw_mixed_batched(const adamw_mixed_tensor_t *tensors, int32_t n_tensors,
+                                  const adamw_mixed_hyper_t *hyper, int32_t step,
+                                  int32_t *step_dev, const float *lr_dev,
+                                  const float *coef_dev, muon_stream_t stream);
+
+/* One gradient of grad_norm_batched: a device array of numel elements, fp32
+ * (4-byte aligned) or bf16 (2-byte aligned); 16-byte aligned arrays take the
+ * vectorised path. */
+typedef struct {
+  const void *grad;
+  int64_t numel;
+  int32_t dtype; /* muon_dtype_t */
+} grad_tensor_t;
+
+/* Norm of all gradients together and the coefficient that clips it:
+ *   out[0] = sqrt(sum of squares);  out[1] = min(1, max_norm / (out[0] + 1e-6)),
+ * squares and sums in 64 bits, each result rounded once to fp32 (a norm past
+ * fp32's range is infinite there, its coefficient is not affected).  If a
+ * gradient is not finite, out[0] is not finite and out[1] is NaN.
+ *  max_norm   > 0; infinite: out[1] is 1 for finite gradients.
+ *  workspace  device, grad_norm_workspace_bytes() bytes, 16-byte aligned,
+ *             zero before its first use; each call leaves it ready for the
+ *             next.  Calls that share a workspace must be ordered, replays of
+ *             captured graphs among them.
+ *  out        device, two floats.
+ * Up to 1300 tensors per launch; at most 2^39 elements per call.
+ * Deterministic on a given GPU. */
+size_t grad_norm_workspace_bytes(void);
+muon_status_t grad_norm_batched(const grad_tensor_t *tensors, int32_t n_tensors,
+                                double max_norm, void *workspace, size_t workspace_bytes,
+                                float *out, muon_stream_t stream);
+
+/* An 8-bit state and plain arrays of its moments (see adam8_write_batched). */
+typedef struct {
+  uint8_t *exp_avg8;
+  uint8_t *root8;
+  uint8_t *scale;
+  void *exp_avg;
+  void *second;
+  int64_t numel;
+} adam8_tensor_t;
+
+/* adam8_write_batched rounds plain moments to 8-bit states (to the nearest),
+ * adam8_read_batched writes out what the states stand for; for checkpoints,
+ * and to move a run from 32-bit states to 8-bit ones or back.  With dtype
+ * MUON_F32, exp_avg and second are fp32 arrays of the first and the second
+ * moment; with MUON_BF16, bf16 arrays of the first moment and of the second
+ * moment's root.  Reading is exact in either type, and writing what was read
+ * back in bf16 gives a state of the same values.  A negative second moment or
+ * root makes its block NaN.  Alignment as in adamw_mixed_tensor_t.  Up to 500
+ * tensors per launch; at most 2^39 elements per call. */
+muon_status_t adam8_write_batched(const adam8_tensor_t *tensors, int32_t n_tensors,
+                                  int32_t dtype, muon_stream_t stream);
+muon_status_t adam8_read_batched(const adam8_tensor_t *tensors, int32_t n_tensors,
+                                 int32_t dtype, muon_stream_t stream);
+
+/* Kernel launches of one call over tensors that are not all empty. */
+int32_t adamw_mixed_launches(int32_t n_tensors);
+int32_t grad_norm_launches(int32_t n_tensors);
+int32_t adam8_launches(int32_t n_tensors);
 
 /* dst[i] = src[i] rounded to bf16 (nearest, ties to even), i < n: one pass
  * over device memory (src fp32, 4-byte aligned; dst bf16 bit patterns,

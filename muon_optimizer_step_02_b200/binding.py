@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 from ctypes import (POINTER, Structure, c_char_p, c_double, c_float, c_int32,
-                    c_int64, c_size_t, c_void_p)
+                    c_int64, c_size_t, c_uint64, c_void_p)
 from typing import List, Optional, Sequence, Tuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -69,6 +69,33 @@ class adamw_hyper_t(Structure):
 class adamw_tensor_t(Structure):
     _fields_ = [("param", c_void_p), ("grad", c_void_p), ("exp_avg", c_void_p),
                 ("exp_avg_sq", c_void_p), ("ema", c_void_p), ("numel", c_int64)]
+
+
+MUON_F32, MUON_BF16 = 0, 1
+_ROUNDINGS = {"nearest": 0, "stochastic": 1}
+ADAM8_BLOCK = 256          # elements that share one pair of scale bytes
+
+
+class adamw_mixed_hyper_t(Structure):
+    _fields_ = [("lr", c_double), ("beta1", c_double), ("beta2", c_double),
+                ("eps", c_double), ("weight_decay", c_double),
+                ("ema_decay", c_double), ("seed", c_uint64), ("rounding", c_int32)]
+
+
+class adamw_mixed_tensor_t(Structure):
+    _fields_ = [("param", c_void_p), ("grad", c_void_p), ("exp_avg", c_void_p),
+                ("exp_avg_sq", c_void_p), ("scale", c_void_p), ("ema", c_void_p),
+                ("copy_bf16", c_void_p), ("numel", c_int64), ("lr_scale", c_float),
+                ("wd_scale", c_float), ("grad_dtype", c_int32)]
+
+
+class grad_tensor_t(Structure):
+    _fields_ = [("grad", c_void_p), ("numel", c_int64), ("dtype", c_int32)]
+
+
+class adam8_tensor_t(Structure):
+    _fields_ = [("exp_avg8", c_void_p), ("root8", c_void_p), ("scale", c_void_p),
+                ("exp_avg", c_void_p), ("second", c_void_p), ("numel", c_int64)]
 
 
 class MuonError(RuntimeError):
@@ -149,6 +176,21 @@ def lib():
     L.muon_noalloc_set_fault.restype = c_int32
     L.muon_f32_to_bf16.argtypes = [c_void_p, c_void_p, c_int64, c_void_p]
     L.muon_f32_to_bf16.restype = c_int32
+    L.adamw_mixed_batched.argtypes = [POINTER(adamw_mixed_tensor_t), c_int32,
+                                      POINTER(adamw_mixed_hyper_t), c_int32,
+                                      c_void_p, c_void_p, c_void_p, c_void_p]
+    L.adamw_mixed_batched.restype = c_int32
+    L.grad_norm_workspace_bytes.argtypes = []
+    L.grad_norm_workspace_bytes.restype = c_size_t
+    L.grad_norm_batched.argtypes = [POINTER(grad_tensor_t), c_int32, c_double,
+                                    c_void_p, c_size_t, c_void_p, c_void_p]
+    L.grad_norm_batched.restype = c_int32
+    for f in (L.adam8_write_batched, L.adam8_read_batched):
+        f.argtypes = [POINTER(adam8_tensor_t), c_int32, c_int32, c_void_p]
+        f.restype = c_int32
+    for f in (L.adamw_mixed_launches, L.grad_norm_launches, L.adam8_launches):
+        f.argtypes = [c_int32]
+        f.restype = c_int32
     L.muon_device_checks.argtypes = []
     L.muon_device_checks.restype = c_int32
     L.muon_device_allocation_count.argtypes = []
@@ -450,6 +492,272 @@ def adamw_ema_batched(params, grads, exp_avgs, exp_avg_sqs, emas, hyper,
 
 def adamw_ema_launches(n_tensors: int, with_step_dev: bool = False) -> int:
     return int(lib().adamw_ema_launches(int(n_tensors), int(bool(with_step_dev))))
+
+
+# ---- AdamW with 32-bit or 8-bit moments --------------------------------------
+
+def _dense(t, dtypes, numel, what, device=None):
+    """Checks a contiguous CUDA tensor of one of `dtypes` with `numel` elements
+    (None: any number) on `device` (None: any); returns it."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{what} has {t.numel()} elements, expected {numel}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what} is on {t.device}, expected {device}")
+    return t
+
+
+def _check_overlap(written, read):
+    """Raises if a written array shares memory with any other array of the
+    call (the same tensor passed twice among them).  Entries: (tensor, name)."""
+    spans = [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), w, name)
+             for w, group in ((True, written), (False, read))
+             for t, name in group if t is not None and t.numel() > 0]
+    spans.sort(key=lambda x: x[:2])
+    end, end_w, name, name_w = 0, 0, "", ""   # furthest ends so far: any span, a written one
+    for b, e, w, what in spans:
+        if b < end_w or (w and b < end):
+            raise ValueError(f"{what} overlaps {name_w if b < end_w else name}")
+        if e > end:
+            end, name = e, what
+        if w and e > end_w:
+            end_w, name_w = e, what
+
+
+def _on_device(fn, device):
+    """fn(stream handle) with `device` current, on `stream` or the device's
+    current stream."""
+    import torch
+
+    def call(stream=None):
+        if stream is not None and getattr(stream, "device", device) != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        if device is None or torch.cuda.current_device() == device.index:
+            return fn(_stream_handle(stream))
+        with torch.cuda.device(device):
+            return fn(_stream_handle(stream))
+    return call
+
+
+class Adam8State:
+    """AdamW's moments of one tensor in 8 bits: codes of the first moment and
+    of the second moment's root (uint8, one per element) and two scale bytes
+    for every ADAM8_BLOCK elements begun.  The three tensors are what a
+    checkpoint keeps; all zero is the state before the first step."""
+
+    def __init__(self, exp_avg, root, scale):
+        import torch
+        n = _dense(exp_avg, (torch.uint8,), None, "exp_avg").numel()
+        _dense(root, (torch.uint8,), n, "root", exp_avg.device)
+        _dense(scale, (torch.uint8,), 2 * self.blocks(n), "scale", exp_avg.device)
+        self.exp_avg, self.root, self.scale, self.numel = exp_avg, root, scale, n
+
+    @staticmethod
+    def blocks(numel: int) -> int:
+        return -(-numel // ADAM8_BLOCK)
+
+    @classmethod
+    def zeros(cls, numel: int, device=None) -> "Adam8State":
+        import torch
+        z = lambda k: torch.zeros(k, dtype=torch.uint8, device=device or "cuda")  # noqa: E731
+        return cls(z(numel), z(numel), z(2 * cls.blocks(numel)))
+
+
+def grad_norm_workspace(device=None):
+    """A workspace of grad_norm_bind: zeroed, 16-byte aligned.  One for every
+    group of calls (captured graphs among them) that are ordered."""
+    import torch
+    return torch.zeros(int(lib().grad_norm_workspace_bytes()), dtype=torch.uint8,
+                       device=device or "cuda")
+
+
+def grad_norm_bind(grads: Sequence, max_norm: float, out, workspace):
+    """Marshals grad_norm_batched once and returns `run(stream=None)`: the norm
+    of all gradients (contiguous fp32 or bf16 CUDA tensors) to out[0] and the
+    coefficient that clips it at max_norm to out[1] (out: two fp32)."""
+    import torch
+    n = len(grads)
+    dev = _dense(out, (torch.float32,), 2, "out").device
+    _dense(workspace, (torch.uint8,), None, "workspace", dev)
+    arr = (grad_tensor_t * max(n, 1))()
+    for i, g in enumerate(grads):
+        _dense(g, (torch.float32, torch.bfloat16), None, f"grads[{i}]", dev)
+        arr[i] = grad_tensor_t(g.data_ptr(), g.numel(),
+                               MUON_BF16 if g.dtype == torch.bfloat16 else MUON_F32)
+    _check_overlap([(out, "out"), (workspace, "workspace")],
+                   [(g, f"grads[{i}]") for i, g in enumerate(grads)])
+    fn = lib().grad_norm_batched
+    keep = (arr, list(grads), out, workspace)
+    limit, ws, ws_n, po = float(max_norm), workspace.data_ptr(), workspace.numel(), out.data_ptr()
+
+    def run(stream):
+        _ = keep
+        _check(fn(arr, n, limit, ws, ws_n, po, stream), "grad_norm_batched")
+    return _on_device(run, dev)
+
+
+def grad_norm_batched(grads, max_norm: float, out, workspace, stream=None):
+    grad_norm_bind(grads, max_norm, out, workspace)(stream)
+
+
+def adamw_mixed_bind(params: Sequence, grads: Sequence, states: Sequence, hyper,
+                     emas: Optional[Sequence] = None, copies: Optional[Sequence] = None,
+                     ema_decay: float = 0.0, step: int = 1, step_dev=None, lr_dev=None,
+                     grad_scale=None, lr_scales: Optional[Sequence[float]] = None,
+                     wd_scales: Optional[Sequence[float]] = None,
+                     rounding: str = "nearest", seed: int = 0):
+    """Marshals adamw_mixed_batched once and returns `run(step_now=None,
+    stream=None)`.  All tensors contiguous, on one CUDA device, none sharing
+    memory with another.
+
+    params: fp32; grads: fp32 or bf16; states[i]: an Adam8State, or a pair
+    (exp_avg, exp_avg_sq) of fp32 tensors; emas[i] (fp32) and copies[i] (bf16,
+    receives the new parameters) may be None, as may the lists.  hyper: an
+    object with lr, beta1, beta2, eps, weight_decay; lr_scales and wd_scales
+    multiply lr and weight_decay per tensor.  With step_dev (two int32, zero
+    before the first step) the device counts the steps; otherwise `step`, or
+    run's `step_now`.  lr_dev: one fp32 read in place of hyper.lr.
+    grad_scale: one fp32 that multiplies the gradients, such as out[1:] of
+    grad_norm_bind; a value that is not finite skips the step.  rounding and
+    seed: how new moments go to 8 bits."""
+    import torch
+    f32, u8 = (torch.float32,), (torch.uint8,)
+    n = len(params)
+    emas = [None] * n if emas is None else list(emas)
+    copies = [None] * n if copies is None else list(copies)
+    lr_scales = [1.0] * n if lr_scales is None else list(lr_scales)
+    wd_scales = [1.0] * n if wd_scales is None else list(wd_scales)
+    if not (len(grads) == len(states) == len(emas) == len(copies) == len(lr_scales)
+            == len(wd_scales) == n):
+        raise ValueError("one grad, state, ema, copy and scale entry per param")
+    if rounding not in _ROUNDINGS:
+        raise ValueError(f"rounding must be one of {sorted(_ROUNDINGS)}, got {rounding!r}")
+    dev = next((t.device for t in (*params, step_dev) if isinstance(t, torch.Tensor)), None)
+    written, read = [], []
+    arr = (adamw_mixed_tensor_t * max(n, 1))()
+    for i in range(n):
+        p = _dense(params[i], f32, None, f"params[{i}]", dev)
+        k = p.numel()
+        g = _dense(grads[i], (torch.float32, torch.bfloat16), k, f"grads[{i}]", dev)
+        if isinstance(states[i], Adam8State):
+            m, v, s = states[i].exp_avg, states[i].root, states[i].scale
+            _dense(m, u8, k, f"states[{i}].exp_avg", dev)
+        else:
+            (m, v), s = states[i], None
+            _dense(m, f32, k, f"states[{i}][0]", dev)
+            _dense(v, f32, k, f"states[{i}][1]", dev)
+        e, c = emas[i], copies[i]
+        if e is not None:
+            _dense(e, f32, k, f"emas[{i}]", dev)
+        if c is not None:
+            _dense(c, (torch.bfloat16,), k, f"copies[{i}]", dev)
+        ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+        arr[i] = adamw_mixed_tensor_t(ptr(p), ptr(g), ptr(m), ptr(v), ptr(s), ptr(e), ptr(c), k,
+                                      float(lr_scales[i]), float(wd_scales[i]),
+                                      MUON_BF16 if g.dtype == torch.bfloat16 else MUON_F32)
+        written += [(p, f"params[{i}]"), (m, f"first moment {i}"), (v, f"second moment {i}"),
+                    (s, f"scale {i}"), (e, f"emas[{i}]"), (c, f"copies[{i}]")]
+        read += [(g, f"grads[{i}]")]
+    for t, dt, k, what in ((step_dev, torch.int32, 2, "step_dev"),
+                           (lr_dev, torch.float32, 1, "lr_dev"),
+                           (grad_scale, torch.float32, 1, "grad_scale")):
+        if t is not None:
+            _dense(t, (dt,), k, what, dev)
+            (written if what == "step_dev" else read).append((t, what))
+    _check_overlap(written, read)
+    hp = adamw_mixed_hyper_t(float(hyper.lr), float(hyper.beta1), float(hyper.beta2),
+                             float(hyper.eps), float(hyper.weight_decay), float(ema_decay),
+                             int(seed) & 0xFFFFFFFFFFFFFFFF, _ROUNDINGS[rounding])
+    hp_ref = ctypes.byref(hp)
+    dptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+    sp, lp, cp = dptr(step_dev), dptr(lr_dev), dptr(grad_scale)
+    fn = lib().adamw_mixed_batched
+    keep = (arr, hp, written, read)
+
+    def run(step_now: Optional[int] = None, stream=None):
+        _ = keep
+        t = int(step if step_now is None else step_now)
+        _on_device(lambda s: _check(fn(arr, n, hp_ref, t, sp, lp, cp, s),
+                                    "adamw_mixed_batched"), dev)(stream)
+    return run
+
+
+def adamw_mixed_batched(params, grads, states, hyper, stream=None, **kw):
+    """One step of adamw_mixed_bind(params, grads, states, hyper, **kw)."""
+    adamw_mixed_bind(params, grads, states, hyper, **kw)(stream=stream)
+
+
+def _adam8_bind(states, exp_avgs, seconds, write: bool):
+    import torch
+    n = len(states)
+    if not (len(exp_avgs) == len(seconds) == n):
+        raise ValueError("one exp_avg and one second entry per state")
+    arr = (adam8_tensor_t * max(n, 1))()
+    dtype = exp_avgs[0].dtype if n else torch.float32
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"plain moments must be torch.float32 or torch.bfloat16, got {dtype}")
+    dev = states[0].exp_avg.device if n else None
+    coded, plain = [], []
+    for i, (s, m, v) in enumerate(zip(states, exp_avgs, seconds)):
+        _dense(s.exp_avg, (torch.uint8,), s.numel, f"states[{i}].exp_avg", dev)
+        _dense(m, (dtype,), s.numel, f"exp_avgs[{i}]", dev)
+        _dense(v, (dtype,), s.numel, f"seconds[{i}]", dev)
+        arr[i] = adam8_tensor_t(s.exp_avg.data_ptr(), s.root.data_ptr(), s.scale.data_ptr(),
+                                m.data_ptr(), v.data_ptr(), s.numel)
+        coded += [(s.exp_avg, f"states[{i}].exp_avg"), (s.root, f"states[{i}].root"),
+                  (s.scale, f"states[{i}].scale")]
+        plain += [(m, f"exp_avgs[{i}]"), (v, f"seconds[{i}]")]
+    _check_overlap(coded if write else plain, plain if write else coded)
+    fn = lib().adam8_write_batched if write else lib().adam8_read_batched
+    what = "adam8_write_batched" if write else "adam8_read_batched"
+    dt = MUON_BF16 if dtype == torch.bfloat16 else MUON_F32
+    keep = (arr, list(states), list(exp_avgs), list(seconds))
+
+    def run(stream):
+        _ = keep
+        _check(fn(arr, n, dt, stream), what)
+    return _on_device(run, dev)
+
+
+def adam8_write_bind(states: Sequence, exp_avgs: Sequence, seconds: Sequence):
+    """Marshals adam8_write_batched once and returns `run(stream=None)`:
+    states[i] (Adam8State) <- plain moments, rounded to the nearest code.
+    fp32 tensors hold the first and the second moment, bf16 tensors the first
+    moment and the second moment's root."""
+    return _adam8_bind(states, exp_avgs, seconds, True)
+
+
+def adam8_read_bind(states: Sequence, exp_avgs: Sequence, seconds: Sequence):
+    """Marshals adam8_read_batched once and returns `run(stream=None)`: plain
+    moments <- what states[i] (Adam8State) stand for, exact in fp32 (first and
+    second moment) and in bf16 (first moment and the second moment's root)."""
+    return _adam8_bind(states, exp_avgs, seconds, False)
+
+
+def adam8_write_batched(states, exp_avgs, seconds, stream=None):
+    adam8_write_bind(states, exp_avgs, seconds)(stream)
+
+
+def adam8_read_batched(states, exp_avgs, seconds, stream=None):
+    adam8_read_bind(states, exp_avgs, seconds)(stream)
+
+
+def adamw_mixed_launches(n_tensors: int) -> int:
+    return int(lib().adamw_mixed_launches(int(n_tensors)))
+
+
+def grad_norm_launches(n_tensors: int) -> int:
+    return int(lib().grad_norm_launches(int(n_tensors)))
+
+
+def adam8_launches(n_tensors: int) -> int:
+    return int(lib().adam8_launches(int(n_tensors)))
 
 
 def ema_launches(n_tensors: int) -> int:
