@@ -531,17 +531,28 @@ def _check_overlap(written, read):
 
 
 def _on_device(fn, device):
-    """fn(stream handle) with `device` current, on `stream` or the device's
-    current stream."""
+    """call(*args, stream=None): fn(*args, stream handle) with `device` current,
+    on `stream` or the device's current stream."""
     import torch
+    if device is None:
+        return lambda *args, stream=None: fn(*args, _stream_handle(stream))
+    index, current_device = device.index, torch.cuda.current_device
+    # the current stream's handle without an object around it (3 us a call)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
-    def call(stream=None):
-        if stream is not None and getattr(stream, "device", device) != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-        if device is None or torch.cuda.current_device() == device.index:
-            return fn(_stream_handle(stream))
-        with torch.cuda.device(device):
-            return fn(_stream_handle(stream))
+    def call(*args, stream=None):
+        if stream is None:
+            handle = raw(index)
+        else:
+            if getattr(stream, "device", device) != device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+            handle = _stream_handle(stream)
+        if current_device() == index:
+            fn(*args, handle)
+        else:
+            with torch.cuda.device(index):
+                fn(*args, handle)
     return call
 
 
@@ -596,10 +607,14 @@ def grad_norm_bind(grads: Sequence, max_norm: float, out, workspace):
     keep = (arr, list(grads), out, workspace)
     limit, ws, ws_n, po = float(max_norm), workspace.data_ptr(), workspace.numel(), out.data_ptr()
 
-    def run(stream):
+    def call(stream):
         _ = keep
         _check(fn(arr, n, limit, ws, ws_n, po, stream), "grad_norm_batched")
-    return _on_device(run, dev)
+    on_device = _on_device(call, dev)
+
+    def run(stream=None):
+        on_device(stream=stream)
+    return run
 
 
 def grad_norm_batched(grads, max_norm: float, out, workspace, stream=None):
@@ -680,11 +695,13 @@ def adamw_mixed_bind(params: Sequence, grads: Sequence, states: Sequence, hyper,
     fn = lib().adamw_mixed_batched
     keep = (arr, hp, written, read)
 
-    def run(step_now: Optional[int] = None, stream=None):
+    def call(t, stream):
         _ = keep
-        t = int(step if step_now is None else step_now)
-        _on_device(lambda s: _check(fn(arr, n, hp_ref, t, sp, lp, cp, s),
-                                    "adamw_mixed_batched"), dev)(stream)
+        _check(fn(arr, n, hp_ref, t, sp, lp, cp, stream), "adamw_mixed_batched")
+    on_device = _on_device(call, dev)
+
+    def run(step_now: Optional[int] = None, stream=None):
+        on_device(int(step if step_now is None else step_now), stream=stream)
     return run
 
 
@@ -719,10 +736,14 @@ def _adam8_bind(states, exp_avgs, seconds, write: bool):
     dt = MUON_BF16 if dtype == torch.bfloat16 else MUON_F32
     keep = (arr, list(states), list(exp_avgs), list(seconds))
 
-    def run(stream):
+    def call(stream):
         _ = keep
         _check(fn(arr, n, dt, stream), what)
-    return _on_device(run, dev)
+    on_device = _on_device(call, dev)
+
+    def run(stream=None):
+        on_device(stream=stream)
+    return run
 
 
 def adam8_write_bind(states: Sequence, exp_avgs: Sequence, seconds: Sequence):

@@ -29,11 +29,17 @@
 
 namespace muonb200 {
 
-constexpr int kMixThreads = 256;
-constexpr int kMixMaxSegs = 400;      // 400 x 80 bytes of kernel parameters (limit 32,764)
+constexpr int kMixThreads = 128;      // 4 warps: a unit of 4 blocks of 256 elements
+constexpr int kMixResident = 6;       // thread blocks per SM (78 registers)
+constexpr int kMixUnit = kMixThreads * 8;
+constexpr int kMixMaxSegs = 400;      // 400 x 76 bytes of kernel parameters (limit 32,764)
 
-constexpr uint32_t kMixGradBf16 = 1;  // gradient is bf16
-constexpr uint32_t kMixVec = 2;       // every array is aligned for 8-element accesses
+// A tensor's element count, its place among the launch's tensors and its flags
+// in one word.
+constexpr unsigned long long kSegBf16 = 1ull << 56;   // gradient (plain moments) in bf16
+constexpr unsigned long long kSegVec = 2ull << 56;    // every array aligned for wide accesses
+constexpr int kSegPlace = 40;
+constexpr unsigned long long kSegNumel = (1ull << kSegPlace) - 1;
 
 struct MixSeg {
   float* p;
@@ -43,70 +49,98 @@ struct MixSeg {
   uint8_t* s;        // scale bytes (m, r) per block; null: fp32 moments
   float* e;          // null: no EMA
   uint16_t* c;       // null: no bf16 copy
-  long long numel;
-  uint32_t ubeg;     // first block of this tensor in the launch's block space
-  uint32_t flags;
+  unsigned long long numel;   // and place, flags
   float lr_scale, wd_scale;
 };
-static_assert(sizeof(MixSeg) == 80, "kMixMaxSegs counts on 80 bytes");
+static_assert(sizeof(MixSeg) == 72, "kMixMaxSegs counts on 72 + 4 bytes");
 
 template <int kSegs>
 struct MixParams {
-  MixSeg seg[kSegs];
-  int32_t* step_dev;        // [0] steps taken, [1] ticket; or null
-  const float* lr_dev;      // or null
-  const float* coef_dev;    // or null
-  double beta1, beta2;
-  int32_t step;             // t when step_dev is null
-  uint32_t key;             // random key before the step number
-  uint32_t n_seg, n_units, first_tensor;
-  int32_t advance;          // this launch advances *step_dev
-  float lr, b1, omb1, b2, omb2, eps, wd, d, omd;
+  MixSeg seg[kSegs];         // those with 8-bit states first
+  uint32_t ubeg[kSegs + 1];  // first unit of each tensor in the launch, and the end
+  uint32_t n_seg, units8;    // units of tensors with 8-bit states
+  int32_t* step_dev;         // [0] steps taken, [1] ticket; or null
+  const float* lr_dev;       // or null
+  const float* coef_dev;     // or null
+  double pow1[31], pow2[31]; // beta^(2^j)
+  int32_t step;              // t when step_dev is null
+  uint32_t key;              // random key before the step number
+  uint32_t first_tensor;
+  int32_t advance;           // this launch advances *step_dev
+  float lr, wd;
+  float one;                 // 1 (see add2)
+  float2 b1, omb1, minus_b2, minus_omb2, eps, d, omd;   // each twice, for two elements
 };
 
-// b^t by squaring: the same products on the host and on the device.
-__host__ __device__ inline double pow_int(double b, uint32_t t) {
-  double r = 1.0;
-  for (; t; t >>= 1) {
-    if (t & 1u) r *= b;
-    b *= b;
-  }
-  return r;
+// Values of 8 elements, two to a register pair: products and sums are issued
+// for two at a time, each rounded as a single one.
+__device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
+
+// A lane's 8 elements of a full block: 4 from place 4 lane on and 4 from
+// 128 + 4 lane on, so that every access of a warp is one stretch of memory.
+// The functions below take the address of the first 4.
+__device__ __forceinline__ void load8(const float* p, float2 (&x)[4]) {
+  const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
+  const float4 b = __ldcs(reinterpret_cast<const float4*>(p + 128));
+  x[0] = make_float2(a.x, a.y);
+  x[1] = make_float2(a.z, a.w);
+  x[2] = make_float2(b.x, b.y);
+  x[3] = make_float2(b.z, b.w);
 }
 
-__device__ __forceinline__ void unpack_bf16x8(const uint4& raw, float (&x)[8]) {
+__device__ __forceinline__ void store8(float* p, const float2 (&x)[4]) {
+  __stcs(reinterpret_cast<float4*>(p), make_float4(x[0].x, x[0].y, x[1].x, x[1].y));
+  __stcs(reinterpret_cast<float4*>(p + 128), make_float4(x[2].x, x[2].y, x[3].x, x[3].y));
+}
+
+__device__ __forceinline__ void unpack8(const uint4& raw, float2 (&x)[4]) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i)
+    x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
 
-__device__ __forceinline__ void load_f32x8(const float* p, float (&x)[8]) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-
-__device__ __forceinline__ void store_f32x8(float* p, const float (&x)[8]) {
-  __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
-  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
-}
-
-__device__ __forceinline__ uint4 pack_bf16x8(const float (&x)[8]) {
-  uint4 o;
-  uint32_t* w = &o.x;
+__device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
+  uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[i].x, x[i].y);
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  return o;
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-constexpr float kMixRootLow = 0x1p-49f, kMixRootHigh = 0x1p63f;
+__device__ __forceinline__ void load8_bf16(const uint16_t* p, float2 (&x)[4]) {
+  const uint2 a = __ldcs(reinterpret_cast<const uint2*>(p));
+  const uint2 b = __ldcs(reinterpret_cast<const uint2*>(p + 128));
+  unpack8(make_uint4(a.x, a.y, b.x, b.y), x);
+}
+
+__device__ __forceinline__ void store8_bf16(uint16_t* p, const float2 (&x)[4]) {
+  const uint4 w = pack8(x);
+  __stcs(reinterpret_cast<uint2*>(p), make_uint2(w.x, w.y));
+  __stcs(reinterpret_cast<uint2*>(p + 128), make_uint2(w.z, w.w));
+}
+
+__device__ __forceinline__ uint2 load8_codes(const uint8_t* p) {
+  return make_uint2(__ldcs(reinterpret_cast<const uint32_t*>(p)),
+                    __ldcs(reinterpret_cast<const uint32_t*>(p + 128)));
+}
+
+__device__ __forceinline__ void store8_codes(uint8_t* p, const uint32_t (&w)[2]) {
+  __stcs(reinterpret_cast<uint32_t*>(p), w[0]);
+  __stcs(reinterpret_cast<uint32_t*>(p + 128), w[1]);
+}
+
+__device__ __forceinline__ float bf16_at(const void* p, long long i) {
+  return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16);
+}
+
+__device__ __forceinline__ float& at(float2 (&x)[4], int k) {
+  return k & 1 ? x[k >> 1].y : x[k >> 1].x;
+}
+
+constexpr float kMixRootLow = 0x1p-49f;
 
 __device__ __forceinline__ float scaled_root(float r, float g, float b2, float omb2, float up,
                                              float down) {
@@ -116,271 +150,565 @@ __device__ __forceinline__ float scaled_root(float r, float g, float b2, float o
   return __fmul_rn(__fsqrt_rn(v), down);
 }
 
-// Last segment whose first block is at or before u.
-template <class Seg>
-__device__ __forceinline__ uint32_t find_seg(const Seg* seg, uint32_t n, uint32_t u) {
+// Largest of three, NaN if one is.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Square roots of two values, given and returned with a minus sign, rounded to
+// the nearest for values in [2^-98, 2^128) (NaN or inexact elsewhere): an
+// estimate s = v y from y = v^(-1/2), and one step of Newton's iteration on
+// its exact residual, s + (v - s^2) y / 2.  The signs let every operation
+// take its operands as they are.
+__device__ __forceinline__ float2 minus_root2(float2 minus_v) {
+  float2 y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(-minus_v.x));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(-minus_v.y));
+  const float2 s = mul2(minus_v, y);
+  return __ffma2_rn(__ffma2_rn(s, s, minus_v), mul2(y, make_float2(0.5f, 0.5f)), s);
+}
+
+// 1 / x to one unit in the last place; x below the normal range counts as 0.
+__device__ __forceinline__ float reciprocal(float x) {
+  float d;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
+  return d;
+}
+
+// The warp's number, in a form that the compiler knows to be the same for all
+// of its lanes, so that what follows from it (blocks, addresses, branches)
+// stays out of the lanes' registers.
+__device__ __forceinline__ int warp_number() {
+  return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+}
+
+// Last tensor whose first unit is at or before u.
+__device__ __forceinline__ uint32_t find_seg(const uint32_t* ubeg, uint32_t n, uint32_t u) {
   uint32_t lo = 0, hi = n - 1;
   while (lo < hi) {
     const uint32_t mid = (lo + hi + 1) >> 1;
-    if (seg[mid].ubeg <= u) lo = mid; else hi = mid - 1;
+    if (ubeg[mid] <= u) lo = mid; else hi = mid - 1;
   }
   return lo;
 }
 
-// One warp per block of 256 elements.  Full blocks of aligned tensors move 8
-// consecutive elements per lane (16-byte accesses, 8-byte ones of codes);
-// others element by element, lane l taking l, l + 32, ...
+// What a launch's tensors share, and one tensor's share of it.
+struct MixStep {
+  float2 coef, minus_rbc2, keep, rate;
+  uint32_t key;    // random key of the tensor
+};
+
+// New moments of a lane's 8 elements from g, m and v (a root for 8-bit states);
+// nr = -r'.  Returns whether some root may be zero.
+template <bool kEight, class P>
+__device__ __forceinline__ bool mixed_moments(const P& a, const MixStep& w, float2 (&g)[4],
+                                              float2 (&m)[4], float2 (&v)[4], float2 (&nr)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    g[k] = mul2(g[k], w.coef);
+    m[k] = add2(mul2(m[k], a.b1), mul2(g[k], a.omb1), a.one);
+    const float2 v0 = kEight ? mul2(v[k], v[k]) : v[k];
+    const float2 nv = add2(mul2(v0, a.minus_b2), mul2(mul2(g[k], g[k]), a.minus_omb2), a.one);
+    nr[k] = minus_root2(nv);
+    if (!kEight) v[k] = make_float2(-nv.x, -nv.y);
+  }
+  // Where r' leaves [2^-49, 2^64) or is no number: the exact root of a 32-bit
+  // state's v'; an 8-bit state holds roots whose squares fp32 does not, and
+  // there r' comes from inputs scaled by a power of two.
+  const float low = max3(max3(max3(max3(nr[0].x, nr[0].y, nr[1].x), nr[1].y, nr[2].x), nr[2].y,
+                              nr[3].x), nr[3].y, nr[3].y);
+  const bool odd = !(low <= -kMixRootLow);
+  if (odd) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float& x = at(nr, k);
+      if (x <= -kMixRootLow) continue;
+      if (!kEight) {
+        x = -__fsqrt_rn(at(v, k));
+        continue;
+      }
+      const float b2 = -a.minus_b2.x, omb2 = -a.minus_omb2.x;
+      x = -scaled_root(at(v, k), at(g, k), b2, omb2, 0x1p70f, 0x1p-70f);
+      if (!isfinite(x)) x = -scaled_root(at(v, k), at(g, k), b2, omb2, 0x1p-70f, 0x1p70f);
+    }
+  }
+  return odd;
+}
+
+// Full blocks with 8-bit states come through shared memory, copied there while
+// the block before is computed.  Each thread copies the pieces that it will
+// read itself, so that no thread waits for another one, in two groups: what
+// the moments need (gradient, codes) is replaced by the next block's as soon
+// as it is read, what the weights need (parameters, averages) likewise, later.
+// Places of the pieces in a thread block's buffer, by thread:
+constexpr int kBufG = 0, kBufCodes = 4096, kBufP = 6144, kBufE = 10240, kMixBuf = 14336;
+
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
+  if (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(kBytes)
+                 : "memory");
+}
+
+// Two pieces of kBytes, 128 elements of kBytes / 4 bytes apart.
+template <int kBytes>
+__device__ __forceinline__ void copy_async2(uint32_t buf, int at, const void* from, int lane) {
+  const uint32_t to = buf + at + threadIdx.x * kBytes;
+  const char* src = static_cast<const char*>(from) + lane * kBytes;
+  copy_async<kBytes>(to, src);
+  copy_async<kBytes>(to + kMixThreads * kBytes, src + 32 * kBytes);
+}
+
+__device__ __forceinline__ float4 from_buf16(uint32_t buf, int at) {
+  float4 x;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(buf + at + threadIdx.x * 16) : "memory");
+  return x;
+}
+
+__device__ __forceinline__ void from_buf8(uint32_t buf, int at, float2 (&x)[4]) {
+  const float4 a = from_buf16(buf, at), b = from_buf16(buf, at + kMixThreads * 16);
+  x[0] = make_float2(a.x, a.y);
+  x[1] = make_float2(a.z, a.w);
+  x[2] = make_float2(b.x, b.y);
+  x[3] = make_float2(b.z, b.w);
+}
+
+__device__ __forceinline__ void from_buf8_bf16(uint32_t buf, int at, float2 (&x)[4]) {
+  uint4 w;
+  const uint32_t p = buf + at + threadIdx.x * 8;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(p) : "memory");
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+               : "=r"(w.z), "=r"(w.w) : "r"(p + kMixThreads * 8) : "memory");
+  unpack8(w, x);
+}
+
+__device__ __forceinline__ uint32_t from_buf4(uint32_t buf, int at) {
+  uint32_t x;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(buf + at + threadIdx.x * 4) : "memory");
+  return x;
+}
+
+template <int kPending>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+__device__ __forceinline__ void copies_group() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// Where a unit's block of this warp lies.
+struct MixPlace {
+  uint32_t cur, end;   // tensor, and its last unit + 1
+  uint32_t blk;
+  long long i0, left;
+  bool full;           // a full block of an aligned tensor
+};
+
+template <class P>
+__device__ __forceinline__ void find_place(const P& a, uint32_t u, int warp, MixPlace& at) {
+  if (u >= at.end) {
+    at.cur = find_seg(a.ubeg, a.n_seg, u);
+    at.end = a.ubeg[at.cur + 1];
+  }
+  const MixSeg& s = a.seg[at.cur];
+  at.blk = (u - a.ubeg[at.cur]) * (kMixUnit / kA8Block) + warp;
+  at.i0 = static_cast<long long>(at.blk) * kA8Block;
+  at.left = static_cast<long long>(s.numel & kSegNumel) - at.i0;
+  at.full = (s.numel & kSegVec) && at.left >= kA8Block;
+}
+
+// Starts the copies that the moments need; returns the scale bytes.
+__device__ __forceinline__ uint32_t fetch_moments(const MixSeg& s, const MixPlace& at,
+                                                  uint32_t buf, int lane) {
+  if (s.numel & kSegBf16)
+    copy_async2<8>(buf, kBufG, static_cast<const uint16_t*>(s.g) + at.i0, lane);
+  else
+    copy_async2<16>(buf, kBufG, static_cast<const float*>(s.g) + at.i0, lane);
+  copy_async2<4>(buf, kBufCodes, static_cast<uint8_t*>(s.m) + at.i0, lane);
+  copy_async2<4>(buf, kBufCodes + 1024, static_cast<uint8_t*>(s.v) + at.i0, lane);
+  return s.s[2ll * at.blk] | static_cast<uint32_t>(s.s[2ll * at.blk + 1]) << 8;
+}
+
+// Starts the copies that the weights need.
+__device__ __forceinline__ void fetch_weights(const MixSeg& s, const MixPlace& at, uint32_t buf,
+                                              int lane) {
+  copy_async2<16>(buf, kBufP, s.p + at.i0, lane);
+  if (s.e) copy_async2<16>(buf, kBufE, s.e + at.i0, lane);
+}
+
+// New weights, averages and copies of a lane's 8 elements.
+template <class P>
+__device__ __forceinline__ void mixed_weights(const P& a, const MixStep& w,
+                                              const float2 (&m)[4], const float2 (&nr)[4],
+                                              float2 (&p)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 den = __ffma2_rn(nr[k], w.minus_rbc2, a.eps);
+    const float2 upd = mul2(m[k], make_float2(reciprocal(den.x), reciprocal(den.y)));
+    p[k] = __ffma2_rn(upd, w.rate, mul2(p[k], w.keep));
+  }
+}
+
+template <class P>
+__device__ __forceinline__ void mixed_average(const P& a, const float2 (&p)[4], float2 (&e)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) e[k] = __ffma2_rn(e[k], a.d, mul2(p[k], a.omd));
+}
+
+// Where a block's element j lies in the warp's part of a piece of the buffer, its elements
+// `size` bytes wide.
+__device__ __forceinline__ uint32_t in_buf(int j, int size) {
+  return (j >> 7) * kMixThreads * 4 * size + ((threadIdx.x & ~31) * 4 + (j & 127)) * size;
+}
+
+// The same for a block that is not full or not aligned: element by element,
+// zeros past the tensor's end.
+__device__ __forceinline__ void fetch_ragged(const MixSeg& s, const MixPlace& at,
+                                             unsigned char* buf, int lane) {
+  __syncwarp();   // the lanes have read the block before
+#pragma unroll
+  for (int j = lane; j < kA8Block; j += 32) {
+    const bool in = j < at.left;
+    const long long i = at.i0 + j;
+    if (s.numel & kSegBf16)
+      *reinterpret_cast<uint16_t*>(buf + kBufG + in_buf(j, 2)) =
+          in ? static_cast<const uint16_t*>(s.g)[i] : 0;
+    else
+      *reinterpret_cast<float*>(buf + kBufG + in_buf(j, 4)) =
+          in ? static_cast<const float*>(s.g)[i] : 0.f;
+    buf[kBufCodes + in_buf(j, 1)] = in ? static_cast<uint8_t*>(s.m)[i] : 0;
+    buf[kBufCodes + 1024 + in_buf(j, 1)] = in ? static_cast<uint8_t*>(s.v)[i] : 0;
+    *reinterpret_cast<float*>(buf + kBufP + in_buf(j, 4)) = in ? s.p[i] : 0.f;
+    if (s.e) *reinterpret_cast<float*>(buf + kBufE + in_buf(j, 4)) = in ? s.e[i] : 0.f;
+  }
+  __syncwarp();
+}
+
+// Element of a lane's k-th value.
+__device__ __forceinline__ int lane_element(int lane, int k) {
+  return lane * 4 + (k & 3) + 128 * (k >> 2);
+}
+
+// A block with an 8-bit state, its copies under way; next_moments and
+// next_weights start the next block's once this one's have been read.
+template <bool kStochastic, bool kG16, class P, class FM, class FW>
+__device__ __forceinline__ void mixed_block8(const P& a, const MixSeg& s, const MixStep& w,
+                                             const MixPlace& at, uint32_t buf, uint32_t scale,
+                                             int lane, const FM& next_moments,
+                                             const FW& next_weights) {
+  const long long i = at.i0 + lane * 4;
+  float2 m[4], nr[4];
+  bool odd;
+  {
+    float2 g[4], r[4];
+    copies_wait<1>();
+    if (kG16) from_buf8_bf16(buf, kBufG, g);
+    else from_buf8(buf, kBufG, g);
+    const float mf = a8_factor(scale & 0xffu), rf = a8_factor(scale >> 8);
+    a8_decode_m4(from_buf4(buf, kBufCodes), mf, m);
+    a8_decode_m4(from_buf4(buf, kBufCodes + 512), mf, m + 2);
+    a8_decode_r4(from_buf4(buf, kBufCodes + 1024), rf, r);
+    a8_decode_r4(from_buf4(buf, kBufCodes + 1536), rf, r + 2);
+    next_moments();
+    odd = mixed_moments<true>(a, w, g, m, r, nr);
+  }
+  {
+    float2 p[4], e[4];
+    copies_wait<1>();
+    from_buf8(buf, kBufP, p);
+    if (s.e) from_buf8(buf, kBufE, e);
+    mixed_weights(a, w, m, nr, p);
+    if (s.e) mixed_average(a, p, e);
+    next_weights();
+    if (at.full) {
+      store8(s.p + i, p);
+      if (s.c) store8_bf16(s.c + i, p);
+      if (s.e) store8(s.e + i, e);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int j = lane_element(lane, k);
+        if (j >= at.left) continue;
+        s.p[at.i0 + j] = ::muonb200::at(p, k);
+        if (s.c) s.c[at.i0 + j] = __bfloat16_as_ushort(__float2bfloat16_rn(::muonb200::at(p, k)));
+        if (s.e) s.e[at.i0 + j] = ::muonb200::at(e, k);
+      }
+    }
+  }
+  if (!at.full) {
+    // past the tensor's end nothing enters the block's largest
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (lane_element(lane, k) >= at.left) ::muonb200::at(m, k) = ::muonb200::at(nr, k) = 0.f;
+    odd = true;
+  }
+  uint32_t word[8], m8[2], r8[2], mbyte, rbyte;
+  if (kStochastic) {
+    // mix32(key of the block ^ element), its first step taken apart: the
+    // element's number (below 256) does not reach the upper half
+    uint32_t bkey = mix32(w.key ^ at.blk);
+    bkey = (bkey ^ (bkey >> 16)) ^ (lane * 4);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      uint32_t x = (bkey ^ ((k & 3) + 128 * (k >> 2))) * 0x57735285u;
+      x = (x ^ (x >> 15)) * 0x4746E6A3u;
+      word[k] = x ^ (x >> 16);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) word[k] = 0u;
+  }
+  a8_encode_block<kStochastic>(m, nr, word, odd, m8, r8, mbyte, rbyte);
+  uint8_t* cm = static_cast<uint8_t*>(s.m);
+  uint8_t* cr = static_cast<uint8_t*>(s.v);
+  if (at.full) {
+    store8_codes(cm + i, m8);
+    store8_codes(cr + i, r8);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int j = lane_element(lane, k);
+      if (j >= at.left) continue;
+      cm[at.i0 + j] = static_cast<uint8_t>(m8[k >> 2] >> (8 * (k & 3)));
+      cr[at.i0 + j] = static_cast<uint8_t>(r8[k >> 2] >> (8 * (k & 3)));
+    }
+  }
+  if (lane == 0) {
+    s.s[2ll * at.blk] = static_cast<uint8_t>(mbyte);
+    s.s[2ll * at.blk + 1] = static_cast<uint8_t>(rbyte);
+  }
+}
+
+// A full block of an aligned tensor with a 32-bit state.
+template <bool kG16, class P>
+__device__ __forceinline__ void mixed_full32(const P& a, const MixSeg& s, const MixStep& w,
+                                             const MixPlace& at, int lane) {
+  const long long i = at.i0 + lane * 4;
+  float2 p[4], g[4], m[4], v[4], nr[4], e[4];
+  load8(static_cast<const float*>(s.m) + i, m);
+  load8(static_cast<const float*>(s.v) + i, v);
+  if (kG16) load8_bf16(static_cast<const uint16_t*>(s.g) + i, g);
+  else load8(static_cast<const float*>(s.g) + i, g);
+  load8(s.p + i, p);
+  if (s.e) load8(s.e + i, e);
+  mixed_moments<false>(a, w, g, m, v, nr);
+  mixed_weights(a, w, m, nr, p);
+  store8(s.p + i, p);
+  if (s.c) store8_bf16(s.c + i, p);
+  if (s.e) {
+    mixed_average(a, p, e);
+    store8(s.e + i, e);
+  }
+  store8(static_cast<float*>(s.m) + i, m);
+  store8(static_cast<float*>(s.v) + i, v);
+}
+
+// Any block with a 32-bit state, element by element: lane l takes l, l + 32, ...
+template <class P>
+__device__ __forceinline__ void mixed_ragged32(const P& a, const MixSeg& s, const MixStep& w,
+                                               const MixPlace& at, int lane) {
+  const bool g16 = (s.numel & kSegBf16) != 0;
+  float2 p[4], g[4], m[4], v[4], nr[4];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int j = k * 32 + lane;
+    const long long i = at.i0 + j;
+    const bool in = j < at.left;
+    ::muonb200::at(p, k) = in ? s.p[i] : 0.f;
+    ::muonb200::at(g, k) = !in ? 0.f : g16 ? bf16_at(s.g, i) : static_cast<const float*>(s.g)[i];
+    ::muonb200::at(m, k) = in ? static_cast<const float*>(s.m)[i] : 0.f;
+    ::muonb200::at(v, k) = in ? static_cast<const float*>(s.v)[i] : 0.f;
+  }
+  mixed_moments<false>(a, w, g, m, v, nr);
+  mixed_weights(a, w, m, nr, p);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int j = k * 32 + lane;
+    const long long i = at.i0 + j;
+    if (j >= at.left) continue;
+    const float x = ::muonb200::at(p, k);
+    s.p[i] = x;
+    if (s.e) s.e[i] = fmaf(s.e[i], a.d.x, __fmul_rn(x, a.omd.x));
+    if (s.c) s.c[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+    static_cast<float*>(s.m)[i] = ::muonb200::at(m, k);
+    static_cast<float*>(s.v)[i] = ::muonb200::at(v, k);
+  }
+}
+
+// A thread block takes a unit of 4 blocks of 256 elements at a time, one warp
+// per block, so that everything about the tensor (table look-up, pointers) is
+// uniform over the thread block.  Full blocks of aligned tensors move in
+// 16-byte accesses (4 or 8 bytes of narrower types); ragged ends and unaligned
+// tensors go element by element.  Tensors with 8-bit states come first, in a
+// loop of their own (one loop for both forms spilled registers).
 template <bool kStochastic, int kSegs>
-__global__ void __launch_bounds__(kMixThreads)
+__global__ void __launch_bounds__(kMixThreads, kMixResident)
 adamw_mixed_kernel(const __grid_constant__ MixParams<kSegs> a) {
+  __shared__ __align__(16) unsigned char s_buf[kMixBuf];
   __shared__ float s_bc[2];
-  __shared__ uint32_t s_t;
-  if (threadIdx.x < 32) {
-    const uint32_t t = a.step_dev ? static_cast<uint32_t>(*a.step_dev) + 1u
-                                  : static_cast<uint32_t>(a.step);
-    const double pw = pow_int(threadIdx.x == 0 ? a.beta1 : a.beta2, t);
-    const double bc = 1.0 / (1.0 - pw);
-    if (threadIdx.x == 0) { s_bc[0] = static_cast<float>(bc); s_t = t; }
-    if (threadIdx.x == 1) s_bc[1] = static_cast<float>(sqrt(bc));
-  }
+  const int lane = threadIdx.x & 31, warp = warp_number();
+  const uint32_t buf = static_cast<uint32_t>(__cvta_generic_to_shared(s_buf));
+  const uint32_t n_units = a.ubeg[a.n_seg];
+  MixPlace next;
+  next.end = 0;
+  next.full = false;
+  uint32_t scale = 0;
+  uint32_t u = blockIdx.x;
+  if (u < a.units8) find_place(a, u, warp, next);
+  if (next.full) scale = fetch_moments(a.seg[next.cur], next, buf, lane);
+  copies_group();
+  if (next.full) fetch_weights(a.seg[next.cur], next, buf, lane);
+  copies_group();
+
+  const uint32_t t = a.step_dev ? static_cast<uint32_t>(*a.step_dev) + 1u
+                                : static_cast<uint32_t>(a.step);
   const float coef = a.coef_dev ? *a.coef_dev : 1.f;
-  const bool skip = !isfinite(coef);
   const float lr0 = a.lr_dev ? *a.lr_dev : a.lr;
-  __syncthreads();
-  if (a.advance && threadIdx.x == 0) {
-    // The last block to have read the count moves it on.
-    __threadfence();
-    const unsigned last = gridDim.x - 1;
-    if (atomicInc(reinterpret_cast<unsigned*>(a.step_dev + 1), last) == last && !skip)
-      *a.step_dev = static_cast<int32_t>(s_t);
+  const bool skip = __any_sync(0xffffffffu, !isfinite(coef));
+  if (threadIdx.x < 32) {
+    const double* pw = threadIdx.x == 0 ? a.pow1 : a.pow2;
+    double x = 1.0;
+    for (uint32_t rest = t; rest; rest &= rest - 1) x *= pw[__ffs(rest) - 1];
+    const float y = static_cast<float>(1.0 - x);
+    if (threadIdx.x == 0) s_bc[0] = __frcp_rn(y);
+    if (threadIdx.x == 1) s_bc[1] = __frcp_rn(__fsqrt_rn(y));
   }
-  if (skip) return;
-  const float bc1 = s_bc[0], rbc2 = s_bc[1];
-  const uint32_t key = kStochastic ? mix32(a.key ^ s_t) : 0u;
+  __syncthreads();   // every thread has read the step count
+  // The last thread block to have read the count moves it on; the ticket's
+  // answer is awaited at the end.
+  const uint32_t last = gridDim.x - 1;
+  uint32_t ticket = last + 1;
+  if (a.advance && threadIdx.x == kMixThreads - 1)
+    asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
+                 : "=r"(ticket) : "l"(a.step_dev + 1), "r"(last) : "memory");
+  if (skip) {
+    copies_wait<0>();
+    return;
+  }
+  const float bc1 = s_bc[0];
+  MixStep w;
+  w.coef = pair(coef);
+  w.minus_rbc2 = pair(-s_bc[1]);
+  const uint32_t key = kStochastic ? mix32(a.key ^ t) : 0u;
 
-  const int lane = threadIdx.x & 31;
-  const uint32_t stride = gridDim.x * (kMixThreads / 32);
-  uint32_t u = blockIdx.x * (kMixThreads / 32) + (threadIdx.x >> 5);
-  if (u >= a.n_units) return;
-  uint32_t cur = find_seg(a.seg, a.n_seg, u);
-  for (; u < a.n_units; u += stride) {
-    while (cur + 1 < a.n_seg && u >= a.seg[cur + 1].ubeg) ++cur;
-    const MixSeg& s = a.seg[cur];
-    const uint32_t blk = u - s.ubeg;
-    const long long i0 = static_cast<long long>(blk) * kA8Block;
-    const long long left = s.numel - i0;
-    const bool vec = (s.flags & kMixVec) && left >= kA8Block;
-    const bool g16 = s.flags & kMixGradBf16;
-    const bool eight = s.s != nullptr;
-    const long long iv = i0 + lane * 8;
-
-    float p[8], g[8], m[8], v[8], e[8];
-    uint32_t mbyte = 0, rbyte = 0;
-    if (eight) {
-      mbyte = s.s[2ll * blk];
-      rbyte = s.s[2ll * blk + 1];
-    }
-    if (vec) {
-      load_f32x8(s.p + iv, p);
-      if (g16) unpack_bf16x8(__ldcs(reinterpret_cast<const uint4*>(
-                                 static_cast<const uint16_t*>(s.g) + iv)), g);
-      else load_f32x8(static_cast<const float*>(s.g) + iv, g);
-      if (s.e) load_f32x8(s.e + iv, e);
-      if (eight) {
-        const uint2 mw = __ldcs(reinterpret_cast<const uint2*>(static_cast<uint8_t*>(s.m) + iv));
-        const uint2 rw = __ldcs(reinterpret_cast<const uint2*>(static_cast<uint8_t*>(s.v) + iv));
-        const float mf = a8_factor(mbyte), rf = a8_factor(rbyte);
-        a8_decode_m4(mw.x, mf, *reinterpret_cast<float(*)[4]>(m));
-        a8_decode_m4(mw.y, mf, *reinterpret_cast<float(*)[4]>(m + 4));
-        a8_decode_r4(rw.x, rf, *reinterpret_cast<float(*)[4]>(v));
-        a8_decode_r4(rw.y, rf, *reinterpret_cast<float(*)[4]>(v + 4));
-      } else {
-        load_f32x8(static_cast<const float*>(s.m) + iv, m);
-        load_f32x8(static_cast<const float*>(s.v) + iv, v);
-      }
-    } else {
-      const float mf = a8_factor(mbyte), rf = a8_factor(rbyte);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int j = k * 32 + lane;
-        const bool in = j < left;
-        const long long i = i0 + j;
-        p[k] = in ? s.p[i] : 0.f;
-        g[k] = !in ? 0.f
-                   : g16 ? __uint_as_float(static_cast<uint32_t>(
-                               static_cast<const uint16_t*>(s.g)[i]) << 16)
-                         : static_cast<const float*>(s.g)[i];
-        e[k] = in && s.e ? s.e[i] : 0.f;
-        if (eight) {
-          float x[4];
-          a8_decode_m4(in ? static_cast<uint8_t*>(s.m)[i] : 0u, mf, x);
-          m[k] = in ? x[0] : 0.f;
-          a8_decode_r4(in ? static_cast<uint8_t*>(s.v)[i] : 0u, rf, x);
-          v[k] = in ? x[0] : 0.f;
-        } else {
-          m[k] = in ? static_cast<const float*>(s.m)[i] : 0.f;
-          v[k] = in ? static_cast<const float*>(s.v)[i] : 0.f;
-        }
-      }
-    }
-
+  const auto set_tensor = [&](const MixSeg& s) {
     const float lr = lr0 * s.lr_scale;
-    const float keep = 1.f - lr * (a.wd * s.wd_scale);
-    float r[8];
-    float rmin = kMixRootLow, rmax = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      g[k] = __fmul_rn(g[k], coef);
-      m[k] = __fadd_rn(__fmul_rn(m[k], a.b1), __fmul_rn(g[k], a.omb1));
-      const float v0 = eight ? __fmul_rn(v[k], v[k]) : v[k];
-      const float v1 = __fadd_rn(__fmul_rn(v0, a.b2), __fmul_rn(__fmul_rn(g[k], g[k]), a.omb2));
-      r[k] = __fsqrt_rn(v1);
-      rmin = fminf(rmin, r[k]);
-      rmax = fmaxf(rmax, r[k]);
-      if (!eight) v[k] = v1;
-    }
-    // An 8-bit state holds roots whose squares fp32 does not: where r' leaves
-    // [2^-49, 2^63], it comes from inputs scaled by a power of two.
-    if (eight && (rmin < kMixRootLow || rmax > kMixRootHigh)) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (r[k] < kMixRootLow)
-          r[k] = scaled_root(v[k], g[k], a.b2, a.omb2, 0x1p70f, 0x1p-70f);
-        else if (r[k] > kMixRootHigh)
-          r[k] = scaled_root(v[k], g[k], a.b2, a.omb2, 0x1p-70f, 0x1p70f);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float upd = __fdividef(m[k] * bc1, fmaf(r[k], rbc2, a.eps));
-      p[k] = fmaf(p[k], keep, -lr * upd);
-      e[k] = fmaf(a.d, e[k], a.omd * p[k]);
-    }
+    w.keep = pair(1.f - lr * (a.wd * s.wd_scale));
+    w.rate = pair(-lr * bc1);
+    if (kStochastic)
+      w.key = mix32(key ^ (a.first_tensor +
+                           (static_cast<uint32_t>(s.numel >> kSegPlace) & 0xffffu)));
+  };
 
-    if (vec) {
-      store_f32x8(s.p + iv, p);
-      if (s.e) store_f32x8(s.e + iv, e);
-      if (s.c) __stcs(reinterpret_cast<uint4*>(s.c + iv), pack_bf16x8(p));
-      if (!eight) {
-        store_f32x8(static_cast<float*>(s.m) + iv, m);
-        store_f32x8(static_cast<float*>(s.v) + iv, v);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int j = k * 32 + lane;
-        if (j >= left) continue;
-        const long long i = i0 + j;
-        s.p[i] = p[k];
-        if (s.e) s.e[i] = e[k];
-        if (s.c) s.c[i] = __bfloat16_as_ushort(__float2bfloat16_rn(p[k]));
-        if (!eight) {
-          static_cast<float*>(s.m)[i] = m[k];
-          static_cast<float*>(s.v)[i] = v[k];
-        }
-      }
+  for (; u < a.units8; u += gridDim.x) {
+    const MixPlace at = next;
+    const MixSeg& s = a.seg[at.cur];
+    set_tensor(s);
+    uint32_t scale_now = scale;
+    next.full = false;
+    if (u + gridDim.x < a.units8) find_place(a, u + gridDim.x, warp, next);
+    const auto next_moments = [&]() {
+      if (next.full) scale = fetch_moments(a.seg[next.cur], next, buf, lane);
+      copies_group();
+    };
+    const auto next_weights = [&]() {
+      if (next.full) fetch_weights(a.seg[next.cur], next, buf, lane);
+      copies_group();
+    };
+    if (at.left <= 0) {
+      next_moments();
+      next_weights();
+      continue;
     }
-    if (eight) {
-      uint32_t word[8], m8[2], r8[2];
-      if (kStochastic) {
-        const uint32_t bkey = mix32(mix32(key ^ (a.first_tensor + cur)) ^ blk);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) word[k] = mix32(bkey ^ (vec ? lane * 8 + k : k * 32 + lane));
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) word[k] = 0u;
-      }
-      if (!vec) {
-        // past the tensor's end nothing enters the block's largest
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k * 32 + lane >= left) m[k] = r[k] = 0.f;
-      }
-      a8_encode_block<kStochastic>(m, r, word, m8, r8, mbyte, rbyte);
-      if (vec) {
-        __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(s.m) + iv),
-               make_uint2(m8[0], m8[1]));
-        __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(s.v) + iv),
-               make_uint2(r8[0], r8[1]));
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int j = k * 32 + lane;
-          if (j >= left) continue;
-          static_cast<uint8_t*>(s.m)[i0 + j] = static_cast<uint8_t>(m8[k >> 2] >> (8 * (k & 3)));
-          static_cast<uint8_t*>(s.v)[i0 + j] = static_cast<uint8_t>(r8[k >> 2] >> (8 * (k & 3)));
-        }
-      }
-      if (lane == 0) {
-        s.s[2ll * blk] = static_cast<uint8_t>(mbyte);
-        s.s[2ll * blk + 1] = static_cast<uint8_t>(rbyte);
-      }
+    if (!at.full) {
+      scale_now = s.s[2ll * at.blk] | static_cast<uint32_t>(s.s[2ll * at.blk + 1]) << 8;
+      fetch_ragged(s, at, s_buf, lane);
+    }
+    if (s.numel & kSegBf16)
+      mixed_block8<kStochastic, true>(a, s, w, at, buf, scale_now, lane, next_moments,
+                                      next_weights);
+    else
+      mixed_block8<kStochastic, false>(a, s, w, at, buf, scale_now, lane, next_moments,
+                                       next_weights);
+  }
+  copies_wait<0>();
+
+  for (; u < n_units; u += gridDim.x) {
+    find_place(a, u, warp, next);
+    const MixSeg& s = a.seg[next.cur];
+    set_tensor(s);
+    if (next.full) {
+      if (s.numel & kSegBf16) mixed_full32<true>(a, s, w, next, lane);
+      else mixed_full32<false>(a, s, w, next, lane);
+    } else if (next.left > 0) {
+      mixed_ragged32(a, s, w, next, lane);
     }
   }
+  if (ticket == last) *a.step_dev = static_cast<int32_t>(t);
 }
 
 // ---- 8-bit states from and to plain arrays --------------------------------
 
-constexpr int kA8MaxSegs = 500;   // 500 x 56 bytes of kernel parameters
+constexpr int kA8MaxSegs = 500;   // 500 x 52 bytes of kernel parameters
 
 struct A8Seg {
   uint8_t *m8, *r8, *s;
-  void* m;          // fp32 or bf16
-  void* v;          // fp32: the second moment; bf16: its root
-  long long numel;
-  uint32_t ubeg;
-  uint32_t flags;   // kMixGradBf16: the plain arrays are bf16; kMixVec
+  void* m;                    // fp32 or bf16
+  void* v;                    // fp32: the second moment; bf16: its root
+  unsigned long long numel;   // and the flags
 };
-static_assert(sizeof(A8Seg) == 56, "kA8MaxSegs counts on 56 bytes");
+static_assert(sizeof(A8Seg) == 48, "kA8MaxSegs counts on 48 + 4 bytes");
 
 template <int kSegs>
 struct A8Params {
   A8Seg seg[kSegs];
-  uint32_t n_seg, n_units;
+  uint32_t ubeg[kSegs + 1];
+  uint32_t n_seg;
 };
 
 // Plain moments -> codes (rounded to the nearest).
 template <int kSegs>
 __global__ void __launch_bounds__(kMixThreads)
 adam8_write_kernel(const __grid_constant__ A8Params<kSegs> a) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t stride = gridDim.x * (kMixThreads / 32);
-  uint32_t u = blockIdx.x * (kMixThreads / 32) + (threadIdx.x >> 5);
-  if (u >= a.n_units) return;
-  uint32_t cur = find_seg(a.seg, a.n_seg, u);
-  for (; u < a.n_units; u += stride) {
-    while (cur + 1 < a.n_seg && u >= a.seg[cur + 1].ubeg) ++cur;
+  const int lane = threadIdx.x & 31, warp = warp_number();
+  const uint32_t n_units = a.ubeg[a.n_seg];
+  uint32_t cur = 0, end = 0;
+  for (uint32_t u = blockIdx.x; u < n_units; u += gridDim.x) {
+    if (u >= end) {
+      cur = find_seg(a.ubeg, a.n_seg, u);
+      end = a.ubeg[cur + 1];
+    }
     const A8Seg& s = a.seg[cur];
-    const uint32_t blk = u - s.ubeg;
+    const uint32_t blk = (u - a.ubeg[cur]) * (kMixUnit / kA8Block) + warp;
     const long long i0 = static_cast<long long>(blk) * kA8Block;
-    const long long left = s.numel - i0;
-    const bool vec = (s.flags & kMixVec) && left >= kA8Block;
-    const bool b16 = s.flags & kMixGradBf16;
-    const long long iv = i0 + lane * 8;
-    float m[8], r[8];
+    const long long left = static_cast<long long>(s.numel & kSegNumel) - i0;
+    if (left <= 0) continue;
+    const bool vec = (s.numel & kSegVec) && left >= kA8Block;
+    const bool b16 = (s.numel & kSegBf16) != 0;
+    const long long iv = i0 + lane * 4;
+    float2 m[4], r[4];
     if (vec) {
       if (b16) {
-        unpack_bf16x8(__ldcs(reinterpret_cast<const uint4*>(static_cast<uint16_t*>(s.m) + iv)), m);
-        unpack_bf16x8(__ldcs(reinterpret_cast<const uint4*>(static_cast<uint16_t*>(s.v) + iv)), r);
+        load8_bf16(static_cast<uint16_t*>(s.m) + iv, m);
+        load8_bf16(static_cast<uint16_t*>(s.v) + iv, r);
       } else {
-        load_f32x8(static_cast<float*>(s.m) + iv, m);
-        load_f32x8(static_cast<float*>(s.v) + iv, r);
+        load8(static_cast<float*>(s.m) + iv, m);
+        load8(static_cast<float*>(s.v) + iv, r);
       }
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int j = k * 32 + lane;
-        const long long i = i0 + j;
-        m[k] = r[k] = 0.f;
-        if (j < left) {
-          if (b16) {
-            m[k] = __uint_as_float(static_cast<uint32_t>(static_cast<uint16_t*>(s.m)[i]) << 16);
-            r[k] = __uint_as_float(static_cast<uint32_t>(static_cast<uint16_t*>(s.v)[i]) << 16);
-          } else {
-            m[k] = static_cast<float*>(s.m)[i];
-            r[k] = static_cast<float*>(s.v)[i];
-          }
-        }
+        const bool in = j < left;
+        at(m, k) = !in ? 0.f : b16 ? bf16_at(s.m, i0 + j) : static_cast<float*>(s.m)[i0 + j];
+        at(r, k) = !in ? 0.f : b16 ? bf16_at(s.v, i0 + j) : static_cast<float*>(s.v)[i0 + j];
       }
     }
     uint32_t word[8], m8[2], r8[2], mbyte, rbyte;
@@ -388,12 +716,15 @@ adam8_write_kernel(const __grid_constant__ A8Params<kSegs> a) {
     for (int k = 0; k < 8; ++k) {
       word[k] = 0u;
       // a second moment (or root) below zero is not one: NaN, like sqrt's
-      r[k] = b16 ? (r[k] < 0.f ? __uint_as_float(0x7fc00000u) : fabsf(r[k])) : fabsf(__fsqrt_rn(r[k]));
+      float& x = at(r, k);
+      if (b16) x = x < 0.f ? __uint_as_float(0x7fc00000u) : x;
+      else x = __fsqrt_rn(x);
+      x = -x;
     }
-    a8_encode_block<false>(m, r, word, m8, r8, mbyte, rbyte);
+    a8_encode_block<false>(m, r, word, true, m8, r8, mbyte, rbyte);
     if (vec) {
-      __stcs(reinterpret_cast<uint2*>(s.m8 + iv), make_uint2(m8[0], m8[1]));
-      __stcs(reinterpret_cast<uint2*>(s.r8 + iv), make_uint2(r8[0], r8[1]));
+      store8_codes(s.m8 + iv, m8);
+      store8_codes(s.r8 + iv, r8);
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -415,37 +746,38 @@ adam8_write_kernel(const __grid_constant__ A8Params<kSegs> a) {
 template <int kSegs>
 __global__ void __launch_bounds__(kMixThreads)
 adam8_read_kernel(const __grid_constant__ A8Params<kSegs> a) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t stride = gridDim.x * (kMixThreads / 32);
-  uint32_t u = blockIdx.x * (kMixThreads / 32) + (threadIdx.x >> 5);
-  if (u >= a.n_units) return;
-  uint32_t cur = find_seg(a.seg, a.n_seg, u);
-  for (; u < a.n_units; u += stride) {
-    while (cur + 1 < a.n_seg && u >= a.seg[cur + 1].ubeg) ++cur;
+  const int lane = threadIdx.x & 31, warp = warp_number();
+  const uint32_t n_units = a.ubeg[a.n_seg];
+  uint32_t cur = 0, end = 0;
+  for (uint32_t u = blockIdx.x; u < n_units; u += gridDim.x) {
+    if (u >= end) {
+      cur = find_seg(a.ubeg, a.n_seg, u);
+      end = a.ubeg[cur + 1];
+    }
     const A8Seg& s = a.seg[cur];
-    const uint32_t blk = u - s.ubeg;
+    const uint32_t blk = (u - a.ubeg[cur]) * (kMixUnit / kA8Block) + warp;
     const long long i0 = static_cast<long long>(blk) * kA8Block;
-    const long long left = s.numel - i0;
-    const bool vec = (s.flags & kMixVec) && left >= kA8Block;
-    const bool b16 = s.flags & kMixGradBf16;
-    const long long iv = i0 + lane * 8;
+    const long long left = static_cast<long long>(s.numel & kSegNumel) - i0;
+    if (left <= 0) continue;
+    const bool vec = (s.numel & kSegVec) && left >= kA8Block;
+    const bool b16 = (s.numel & kSegBf16) != 0;
+    const long long iv = i0 + lane * 4;
     const float mf = a8_factor(s.s[2ll * blk]), rf = a8_factor(s.s[2ll * blk + 1]);
-    float m[8], r[8];
+    float2 m[4], r[4];
     if (vec) {
-      const uint2 mw = __ldcs(reinterpret_cast<const uint2*>(s.m8 + iv));
-      const uint2 rw = __ldcs(reinterpret_cast<const uint2*>(s.r8 + iv));
-      a8_decode_m4(mw.x, mf, *reinterpret_cast<float(*)[4]>(m));
-      a8_decode_m4(mw.y, mf, *reinterpret_cast<float(*)[4]>(m + 4));
-      a8_decode_r4(rw.x, rf, *reinterpret_cast<float(*)[4]>(r));
-      a8_decode_r4(rw.y, rf, *reinterpret_cast<float(*)[4]>(r + 4));
+      const uint2 mw = load8_codes(s.m8 + iv), rw = load8_codes(s.r8 + iv);
+      a8_decode_m4(mw.x, mf, m);
+      a8_decode_m4(mw.y, mf, m + 2);
+      a8_decode_r4(rw.x, rf, r);
+      a8_decode_r4(rw.y, rf, r + 2);
       if (b16) {
-        __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(s.m) + iv), pack_bf16x8(m));
-        __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(s.v) + iv), pack_bf16x8(r));
+        store8_bf16(static_cast<uint16_t*>(s.m) + iv, m);
+        store8_bf16(static_cast<uint16_t*>(s.v) + iv, r);
       } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) r[k] *= r[k];
-        store_f32x8(static_cast<float*>(s.m) + iv, m);
-        store_f32x8(static_cast<float*>(s.v) + iv, r);
+        for (int k = 0; k < 4; ++k) r[k] = mul2(r[k], r[k]);
+        store8(static_cast<float*>(s.m) + iv, m);
+        store8(static_cast<float*>(s.v) + iv, r);
       }
     } else {
 #pragma unroll
@@ -453,15 +785,15 @@ adam8_read_kernel(const __grid_constant__ A8Params<kSegs> a) {
         const int j = k * 32 + lane;
         if (j >= left) continue;
         const long long i = i0 + j;
-        float x[4], y[4];
+        float2 x[2], y[2];
         a8_decode_m4(s.m8[i], mf, x);
         a8_decode_r4(s.r8[i], rf, y);
         if (b16) {
-          static_cast<uint16_t*>(s.m)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x[0]));
-          static_cast<uint16_t*>(s.v)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(y[0]));
+          static_cast<uint16_t*>(s.m)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x[0].x));
+          static_cast<uint16_t*>(s.v)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(y[0].x));
         } else {
-          static_cast<float*>(s.m)[i] = x[0];
-          static_cast<float*>(s.v)[i] = y[0] * y[0];
+          static_cast<float*>(s.m)[i] = x[0].x;
+          static_cast<float*>(s.v)[i] = y[0].x * y[0].x;
         }
       }
     }

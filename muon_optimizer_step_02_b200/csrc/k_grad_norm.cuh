@@ -23,16 +23,17 @@
 namespace muonb200 {
 
 constexpr int kNormThreads = 256;
-constexpr int kNormMaxSegs = 1300;    // 1300 x 24 bytes of kernel parameters
+constexpr int kNormChunk = kNormThreads * 8;
+constexpr int kNormDeep = 4;          // chunks of a unit, all requested at once
+constexpr int kNormUnit = kNormDeep * kNormChunk;
+constexpr int kNormResident = 8;      // thread blocks per SM (32 registers)
+constexpr int kNormMaxSegs = 1300;    // 1300 x 20 bytes of kernel parameters
 constexpr int kNormMaxGrid = 2048;
 
 struct NormSeg {
   const void* g;
-  long long numel;
-  uint32_t ubeg;
-  uint32_t flags;    // kMixGradBf16, kMixVec
+  unsigned long long numel;   // and the flags kSegBf16, kSegVec
 };
-static_assert(sizeof(NormSeg) == 24, "kNormMaxSegs counts on 24 bytes");
 
 struct NormWorkspace {
   unsigned ticket;   // 0 between calls
@@ -44,10 +45,11 @@ struct NormWorkspace {
 template <int kSegs>
 struct NormParams {
   NormSeg seg[kSegs];
+  uint32_t ubeg[kSegs + 1];  // first unit of each tensor in the launch, and the end
+  uint32_t n_seg;
   NormWorkspace* ws;
   float* out;               // norm, coefficient
   double max_norm;
-  uint32_t n_seg, n_units;
   int32_t first, last;      // first / last launch of the call
 };
 
@@ -62,47 +64,92 @@ __device__ __forceinline__ double block_sum(double x, double* sh) {
   return x;
 }
 
+__device__ __forceinline__ void add_squares(const float2 (&g)[4], double (&sum)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const double x = static_cast<double>(g[k].x), y = static_cast<double>(g[k].y);
+    sum[k] = fma(x, x, sum[k]);
+    sum[k] = fma(y, y, sum[k]);
+  }
+}
+
+// kCount whole chunks of an aligned gradient from element i0 on, requested
+// before the first is used.
+template <int kCount, bool kG16>
+__device__ __forceinline__ void add_chunks(const void* g, long long i0, double (&sum)[4]) {
+  float2 x[4];
+  if (kG16) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g) + i0) +
+                     threadIdx.x;
+    uint4 raw[kCount];
+#pragma unroll
+    for (int c = 0; c < kCount; ++c) raw[c] = __ldcs(p + c * kNormThreads);
+#pragma unroll
+    for (int c = 0; c < kCount; ++c) {
+      unpack8(raw[c], x);
+      add_squares(x, sum);
+    }
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(g) + i0) +
+                      threadIdx.x;
+    float4 raw[2 * kCount];
+#pragma unroll
+    for (int c = 0; c < 2 * kCount; ++c) raw[c] = __ldcs(p + c * kNormThreads);
+#pragma unroll
+    for (int c = 0; c < kCount; ++c) {
+      x[0] = make_float2(raw[2 * c].x, raw[2 * c].y);
+      x[1] = make_float2(raw[2 * c].z, raw[2 * c].w);
+      x[2] = make_float2(raw[2 * c + 1].x, raw[2 * c + 1].y);
+      x[3] = make_float2(raw[2 * c + 1].z, raw[2 * c + 1].w);
+      add_squares(x, sum);
+    }
+  }
+}
+
 template <int kSegs>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(kNormThreads, kNormResident)
 grad_norm_kernel(const __grid_constant__ NormParams<kSegs> a) {
   __shared__ double sh[2][kNormThreads / 32];
   __shared__ bool s_last;
-  const int lane = threadIdx.x & 31;
-  const uint32_t stride = gridDim.x * (kNormThreads / 32);
-  uint32_t u = blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5);
-  double sum = 0.0;
-  if (u < a.n_units) {
-    uint32_t cur = find_seg(a.seg, a.n_seg, u);
-    for (; u < a.n_units; u += stride) {
-      while (cur + 1 < a.n_seg && u >= a.seg[cur + 1].ubeg) ++cur;
-      const NormSeg& s = a.seg[cur];
-      const long long i0 = static_cast<long long>(u - s.ubeg) * kA8Block;
-      const long long left = s.numel - i0;
-      const bool vec = (s.flags & kMixVec) && left >= kA8Block;
-      const bool g16 = s.flags & kMixGradBf16;
-      float g[8];
-      if (vec) {
-        const long long iv = i0 + lane * 8;
-        if (g16) unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(
-                                   static_cast<const uint16_t*>(s.g) + iv)), g);
-        else load_f32x8(static_cast<const float*>(s.g) + iv, g);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int j = k * 32 + lane;
-          g[k] = j >= left ? 0.f
-                 : g16     ? __uint_as_float(static_cast<uint32_t>(
-                             static_cast<const uint16_t*>(s.g)[i0 + j]) << 16)
-                           : static_cast<const float*>(s.g)[i0 + j];
-        }
+  const uint32_t n_units = a.ubeg[a.n_seg];
+  uint32_t cur = 0, end = 0;
+  double sum[4] = {0.0, 0.0, 0.0, 0.0};
+  for (uint32_t u = blockIdx.x; u < n_units; u += gridDim.x) {
+    if (u >= end) {
+      cur = find_seg(a.ubeg, a.n_seg, u);
+      end = a.ubeg[cur + 1];
+    }
+    const NormSeg& s = a.seg[cur];
+    long long i0 = static_cast<long long>(u - a.ubeg[cur]) * kNormUnit;
+    long long left = static_cast<long long>(s.numel & kSegNumel) - i0;
+    const bool g16 = (s.numel & kSegBf16) != 0;
+    const bool vec = (s.numel & kSegVec) != 0;
+    if (vec && left >= kNormUnit) {
+      if (g16) add_chunks<kNormDeep, true>(s.g, i0, sum);
+      else add_chunks<kNormDeep, false>(s.g, i0, sum);
+      continue;
+    }
+    // a tensor's last unit, or one that is not aligned: chunk by chunk
+    for (int c = 0; c < kNormDeep && left > 0; ++c, i0 += kNormChunk, left -= kNormChunk) {
+      if (vec && left >= kNormChunk) {
+        if (g16) add_chunks<1, true>(s.g, i0, sum);
+        else add_chunks<1, false>(s.g, i0, sum);
+        continue;
       }
+      float2 g[4];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum = fma(static_cast<double>(g[k]), static_cast<double>(g[k]), sum);
+      for (int k = 0; k < 8; ++k) {
+        const int j = k * kNormThreads + threadIdx.x;
+        at(g, k) = j >= left ? 0.f
+                   : g16     ? bf16_at(s.g, i0 + j)
+                             : static_cast<const float*>(s.g)[i0 + j];
+      }
+      add_squares(g, sum);
     }
   }
-  sum = block_sum(sum, sh[0]);
+  double total = block_sum((sum[0] + sum[1]) + (sum[2] + sum[3]), sh[0]);
   if (threadIdx.x == 0) {
-    a.ws->part[blockIdx.x] = sum;
+    a.ws->part[blockIdx.x] = total;
     __threadfence();
     s_last = atomicInc(&a.ws->ticket, gridDim.x - 1) == gridDim.x - 1;
   }

@@ -22,8 +22,12 @@ constexpr int kFewSegs = 16;   // launches of few tensors carry a short table
 
 inline uintptr_t bits(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 
-inline uint32_t blocks_of(int64_t numel) {
-  return static_cast<uint32_t>((numel + kA8Block - 1) / kA8Block);
+inline uint32_t units_of(int64_t numel, int unit) {
+  return static_cast<uint32_t>((numel + unit - 1) / unit);
+}
+
+inline unsigned long long flagged(int64_t numel, bool bf16, bool vec) {
+  return static_cast<unsigned long long>(numel) | (bf16 ? kSegBf16 : 0) | (vec ? kSegVec : 0);
 }
 
 inline muon_status_t sm_count(int& sms) {
@@ -34,17 +38,21 @@ inline muon_status_t sm_count(int& sms) {
   return MUON_OK;
 }
 
-// One warp per block of 256 elements; at least one thread block, so that an
-// empty call still advances its counter or writes its norm.
+// At least one thread block, so that an empty call still advances its counter
+// or writes its norm.
 inline unsigned grid_for(uint32_t units, int sms, int blocks_per_sm) {
-  const uint32_t want = (units + 7u) / 8u;
-  return std::max(1u, std::min(want, static_cast<unsigned>(blocks_per_sm * sms)));
+  return std::max(1u, std::min(units, static_cast<unsigned>(blocks_per_sm * sms)));
+}
+
+inline float2 twice(double x) {
+  return make_float2(static_cast<float>(x), static_cast<float>(x));
 }
 
 template <class P>
-muon_status_t launch(void (*kernel)(P), const P& params, unsigned grid, cudaStream_t st) {
+muon_status_t launch(void (*kernel)(P), const P& params, unsigned grid, int threads,
+                     cudaStream_t st) {
   void* args[] = {const_cast<P*>(&params)};
-  if (cudaLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(grid), dim3(kMixThreads),
+  if (cudaLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(grid), dim3(threads),
                        args, 0, st) != cudaSuccess) {
     cudaGetLastError();
     return MUON_ERR_CUDA;
@@ -61,39 +69,53 @@ muon_status_t mixed_launch(const adamw_mixed_tensor_t* x, int first, int n,
   a.step_dev = step_dev;
   a.lr_dev = lr_dev;
   a.coef_dev = coef_dev;
-  a.beta1 = h.beta1;
-  a.beta2 = h.beta2;
   a.step = step;
   a.key = mix32(mix32(static_cast<uint32_t>(h.seed)) ^ static_cast<uint32_t>(h.seed >> 32));
   a.first_tensor = static_cast<uint32_t>(first);
   a.advance = advance ? 1 : 0;
   a.lr = static_cast<float>(h.lr);
-  a.b1 = static_cast<float>(h.beta1);
-  a.omb1 = static_cast<float>(1.0 - h.beta1);
-  a.b2 = static_cast<float>(h.beta2);
-  a.omb2 = static_cast<float>(1.0 - h.beta2);
-  a.eps = static_cast<float>(h.eps);
+  a.b1 = twice(h.beta1);
+  a.omb1 = twice(1.0 - h.beta1);
+  a.minus_b2 = twice(-h.beta2);
+  a.minus_omb2 = twice(-(1.0 - h.beta2));
+  a.eps = twice(h.eps);
   a.wd = static_cast<float>(h.weight_decay);
-  a.d = static_cast<float>(h.ema_decay);
-  a.omd = static_cast<float>(1.0 - h.ema_decay);
+  a.d = twice(h.ema_decay);
+  a.omd = twice(1.0 - h.ema_decay);
+  a.one = 1.f;
+  a.pow1[0] = h.beta1;
+  a.pow2[0] = h.beta2;
+  for (int j = 1; j < 31; ++j) {
+    a.pow1[j] = a.pow1[j - 1] * a.pow1[j - 1];
+    a.pow2[j] = a.pow2[j - 1] * a.pow2[j - 1];
+  }
   uint32_t units = 0;
-  for (int i = 0; i < n; ++i) {
-    const adamw_mixed_tensor_t& t = x[first + i];
-    const bool g16 = t.grad_dtype == MUON_BF16;
-    const uintptr_t wide = bits(t.param) | bits(t.grad) | bits(t.ema) | bits(t.copy_bf16);
-    const uintptr_t state = bits(t.exp_avg) | bits(t.exp_avg_sq);
-    const bool vec = (wide & 15u) == 0 && (state & (t.scale ? 7u : 15u)) == 0;
-    a.seg[i] = MixSeg{t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.scale, t.ema, t.copy_bf16,
-                      t.numel, units, (g16 ? kMixGradBf16 : 0u) | (vec ? kMixVec : 0u),
-                      t.lr_scale, t.wd_scale};
-    units += blocks_of(t.numel);
+  int k = 0;
+  for (int eight = 1; eight >= 0; --eight) {
+    for (int i = 0; i < n; ++i) {
+      const adamw_mixed_tensor_t& t = x[first + i];
+      if ((t.scale != nullptr) != (eight == 1)) continue;
+      const uintptr_t wide = bits(t.param) | bits(t.ema);
+      const bool g16 = t.grad_dtype == MUON_BF16;
+      const uintptr_t codes = bits(t.exp_avg) | bits(t.exp_avg_sq);
+      const bool vec = ((wide | (eight ? 0 : codes) | (g16 ? 0 : bits(t.grad))) & 15u) == 0 &&
+                       ((bits(t.copy_bf16) | (g16 ? bits(t.grad) : 0)) & 7u) == 0 &&
+                       (codes & 3u) == 0;
+      a.seg[k] = MixSeg{t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.scale, t.ema, t.copy_bf16,
+                        flagged(t.numel, g16, vec) |
+                            static_cast<unsigned long long>(i) << kSegPlace,
+                        t.lr_scale, t.wd_scale};
+      a.ubeg[k++] = units;
+      units += units_of(t.numel, kMixUnit);
+    }
+    if (eight) a.units8 = units;
   }
   a.n_seg = static_cast<uint32_t>(n);
-  a.n_units = units;
-  const unsigned grid = grid_for(units, sms, 8);
+  a.ubeg[n] = units;
+  const unsigned grid = grid_for(units, sms, kMixResident);
   return h.rounding == MUON_ROUND_STOCHASTIC
-             ? launch(adamw_mixed_kernel<true, kSegs>, a, grid, st)
-             : launch(adamw_mixed_kernel<false, kSegs>, a, grid, st);
+             ? launch(adamw_mixed_kernel<true, kSegs>, a, grid, kMixThreads, st)
+             : launch(adamw_mixed_kernel<false, kSegs>, a, grid, kMixThreads, st);
 }
 
 template <int kSegs>
@@ -108,14 +130,14 @@ muon_status_t norm_launch(const grad_tensor_t* x, int n, double max_norm, NormWo
   uint32_t units = 0;
   for (int i = 0; i < n; ++i) {
     const bool g16 = x[i].dtype == MUON_BF16;
-    a.seg[i] = NormSeg{x[i].grad, x[i].numel, units,
-                       (g16 ? kMixGradBf16 : 0u) | ((bits(x[i].grad) & 15u) ? 0u : kMixVec)};
-    units += blocks_of(x[i].numel);
+    a.seg[i] = NormSeg{x[i].grad, flagged(x[i].numel, g16, (bits(x[i].grad) & 15u) == 0)};
+    a.ubeg[i] = units;
+    units += units_of(x[i].numel, kNormUnit);
   }
   a.n_seg = static_cast<uint32_t>(n);
-  a.n_units = units;
-  const unsigned grid = std::min<unsigned>(grid_for(units, sms, 8), kNormMaxGrid);
-  return launch(grad_norm_kernel<kSegs>, a, grid, st);
+  a.ubeg[n] = units;
+  const unsigned grid = std::min<unsigned>(grid_for(units, sms, kNormResident), kNormMaxGrid);
+  return launch(grad_norm_kernel<kSegs>, a, grid, kNormThreads, st);
 }
 
 template <int kSegs>
@@ -125,18 +147,20 @@ muon_status_t adam8_launch(const adam8_tensor_t* x, int n, int32_t dtype, bool w
   uint32_t units = 0;
   for (int i = 0; i < n; ++i) {
     const adam8_tensor_t& t = x[i];
-    const bool vec = ((bits(t.exp_avg) | bits(t.second)) & 15u) == 0 &&
-                     ((bits(t.exp_avg8) | bits(t.root8)) & 7u) == 0;
-    a.seg[i] = A8Seg{t.exp_avg8, t.root8, t.scale, t.exp_avg, t.second, t.numel, units,
-                     (dtype == MUON_BF16 ? kMixGradBf16 : 0u) | (vec ? kMixVec : 0u)};
-    units += blocks_of(t.numel);
+    const bool vec =
+        ((bits(t.exp_avg) | bits(t.second)) & (dtype == MUON_BF16 ? 7u : 15u)) == 0 &&
+        ((bits(t.exp_avg8) | bits(t.root8)) & 3u) == 0;
+    a.seg[i] = A8Seg{t.exp_avg8, t.root8, t.scale, t.exp_avg, t.second,
+                     flagged(t.numel, dtype == MUON_BF16, vec)};
+    a.ubeg[i] = units;
+    units += units_of(t.numel, kMixUnit);
   }
   if (units == 0) return MUON_OK;
   a.n_seg = static_cast<uint32_t>(n);
-  a.n_units = units;
-  const unsigned grid = grid_for(units, sms, 8);
-  return write ? launch(adam8_write_kernel<kSegs>, a, grid, st)
-               : launch(adam8_read_kernel<kSegs>, a, grid, st);
+  a.ubeg[n] = units;
+  const unsigned grid = grid_for(units, sms, 16);
+  return write ? launch(adam8_write_kernel<kSegs>, a, grid, kMixThreads, st)
+               : launch(adam8_read_kernel<kSegs>, a, grid, kMixThreads, st);
 }
 
 muon_status_t adam8_convert(const adam8_tensor_t* tensors, int32_t n_tensors, int32_t dtype,
