@@ -146,11 +146,12 @@ __device__ __forceinline__ uint32_t upper_halves(uint32_t a, uint32_t b) {
 
 // Encodes a lane's 8 elements of both moments; the warp holds one block.
 // m: first moments, nr: roots with a minus sign (both 0 past the tensor's
-// end); word: per element 32 random bits (the lower half for m, the upper for
-// r); zeros: whether some of the lane's roots may be zero.
+// end); x: per element the 32 random bits before mix32's last step, which
+// leaves their upper half (for r) as it is and joins it to the lower (for m);
+// zeros: whether some of the lane's roots may be zero.
 template <bool kStochastic>
 __device__ __forceinline__ void a8_encode_block(const float2 (&m)[4], const float2 (&nr)[4],
-                                                const uint32_t (&word)[8], bool zeros,
+                                                const uint32_t (&x)[8], bool zeros,
                                                 uint32_t (&m8)[2], uint32_t (&r8)[2],
                                                 uint32_t& mbyte, uint32_t& rbyte) {
   mbyte = a8_scale_byte<kA8MBits>(warp_largest(m));
@@ -161,17 +162,18 @@ __device__ __forceinline__ void a8_encode_block(const float2 (&m)[4], const floa
   uint32_t mh[4], rh[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
+    const uint32_t h0 = x[2 * k] >> 16, h1 = x[2 * k + 1] >> 16;
     // sign in bit 31, code in bits 25..19
-    mh[k] = upper_halves(
-        a8_round<kA8MBits, kStochastic>(__float_as_uint(ms[k].x), word[2 * k] & 0xffffu),
-        a8_round<kA8MBits, kStochastic>(__float_as_uint(ms[k].y), word[2 * k + 1] & 0xffffu));
+    mh[k] = upper_halves(a8_round<kA8MBits, kStochastic>(__float_as_uint(ms[k].x),
+                                                         (x[2 * k] ^ h0) & 0xffffu),
+                         a8_round<kA8MBits, kStochastic>(__float_as_uint(ms[k].y),
+                                                         (x[2 * k + 1] ^ h1) & 0xffffu));
     // a root above zero starts from code 1's pattern at least; code in bits 25..18
     constexpr float kOne = 0x1p-131f;
     static_assert(kA8RBits == 5, "kOne is code 1's pattern, 1 << 18");
-    rh[k] = upper_halves(a8_round<kA8RBits, kStochastic>(
-                             __float_as_uint(fmaxf(rs[k].x, kOne)), word[2 * k] >> 16),
-                         a8_round<kA8RBits, kStochastic>(
-                             __float_as_uint(fmaxf(rs[k].y, kOne)), word[2 * k + 1] >> 16));
+    rh[k] = upper_halves(
+        a8_round<kA8RBits, kStochastic>(__float_as_uint(fmaxf(rs[k].x, kOne)), h0),
+        a8_round<kA8RBits, kStochastic>(__float_as_uint(fmaxf(rs[k].y, kOne)), h1));
     if (zeros) {
       if (nr[k].x == 0.f) rh[k] &= 0xffff0000u;
       if (nr[k].y == 0.f) rh[k] &= 0x0000ffffu;

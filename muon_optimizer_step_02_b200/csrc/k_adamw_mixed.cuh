@@ -76,21 +76,20 @@ struct MixParams {
 // for two at a time, each rounded as a single one.
 __device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
 
-// A lane's 8 elements of a full block: 4 from place 4 lane on and 4 from
-// 128 + 4 lane on, so that every access of a warp is one stretch of memory.
-// The functions below take the address of the first 4.
+// A lane's 8 elements of a full block, 8 lane to 8 lane + 7: 32 bytes of fp32
+// in one access, 16 of bf16, 8 of codes.
 __device__ __forceinline__ void load8(const float* p, float2 (&x)[4]) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldcs(reinterpret_cast<const float4*>(p + 128));
-  x[0] = make_float2(a.x, a.y);
-  x[1] = make_float2(a.z, a.w);
-  x[2] = make_float2(b.x, b.y);
-  x[3] = make_float2(b.z, b.w);
+  asm volatile("ld.global.cs.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(x[0].x), "=f"(x[0].y), "=f"(x[1].x), "=f"(x[1].y), "=f"(x[2].x),
+                 "=f"(x[2].y), "=f"(x[3].x), "=f"(x[3].y)
+               : "l"(p));
 }
 
 __device__ __forceinline__ void store8(float* p, const float2 (&x)[4]) {
-  __stcs(reinterpret_cast<float4*>(p), make_float4(x[0].x, x[0].y, x[1].x, x[1].y));
-  __stcs(reinterpret_cast<float4*>(p + 128), make_float4(x[2].x, x[2].y, x[3].x, x[3].y));
+  asm volatile("st.global.cs.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
+               "f"(x[0].x), "f"(x[0].y), "f"(x[1].x), "f"(x[1].y), "f"(x[2].x), "f"(x[2].y),
+               "f"(x[3].x), "f"(x[3].y)
+               : "memory");
 }
 
 __device__ __forceinline__ void unpack8(const uint4& raw, float2 (&x)[4]) {
@@ -111,25 +110,19 @@ __device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
 }
 
 __device__ __forceinline__ void load8_bf16(const uint16_t* p, float2 (&x)[4]) {
-  const uint2 a = __ldcs(reinterpret_cast<const uint2*>(p));
-  const uint2 b = __ldcs(reinterpret_cast<const uint2*>(p + 128));
-  unpack8(make_uint4(a.x, a.y, b.x, b.y), x);
+  unpack8(__ldcs(reinterpret_cast<const uint4*>(p)), x);
 }
 
 __device__ __forceinline__ void store8_bf16(uint16_t* p, const float2 (&x)[4]) {
-  const uint4 w = pack8(x);
-  __stcs(reinterpret_cast<uint2*>(p), make_uint2(w.x, w.y));
-  __stcs(reinterpret_cast<uint2*>(p + 128), make_uint2(w.z, w.w));
+  __stcs(reinterpret_cast<uint4*>(p), pack8(x));
 }
 
 __device__ __forceinline__ uint2 load8_codes(const uint8_t* p) {
-  return make_uint2(__ldcs(reinterpret_cast<const uint32_t*>(p)),
-                    __ldcs(reinterpret_cast<const uint32_t*>(p + 128)));
+  return __ldcs(reinterpret_cast<const uint2*>(p));
 }
 
 __device__ __forceinline__ void store8_codes(uint8_t* p, const uint32_t (&w)[2]) {
-  __stcs(reinterpret_cast<uint32_t*>(p), w[0]);
-  __stcs(reinterpret_cast<uint32_t*>(p + 128), w[1]);
+  __stcs(reinterpret_cast<uint2*>(p), make_uint2(w[0], w[1]));
 }
 
 __device__ __forceinline__ float bf16_at(const void* p, long long i) {
@@ -238,11 +231,12 @@ __device__ __forceinline__ bool mixed_moments(const P& a, const MixStep& w, floa
 }
 
 // Full blocks with 8-bit states come through shared memory, copied there while
-// the block before is computed.  Each thread copies the pieces that it will
-// read itself, so that no thread waits for another one, in two groups: what
-// the moments need (gradient, codes) is replaced by the next block's as soon
-// as it is read, what the weights need (parameters, averages) likewise, later.
-// Places of the pieces in a thread block's buffer, by thread:
+// the block before is computed, in two groups: what the moments need
+// (gradient, codes) is replaced by the next block's as soon as it is read,
+// what the weights need (parameters, averages) likewise, later.  fp32 arrays
+// are copied in 16-byte pieces, lane l taking pieces l and 32 + l (so that a
+// warp's access is one stretch of memory) where it reads 2 l and 2 l + 1; the
+// other arrays by the lane that will read them.  Places in a thread block's buffer:
 constexpr int kBufG = 0, kBufCodes = 4096, kBufP = 6144, kBufE = 10240, kMixBuf = 14336;
 
 template <int kBytes>
@@ -254,49 +248,42 @@ __device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
                  : "memory");
 }
 
-// Two pieces of kBytes, 128 elements of kBytes / 4 bytes apart.
-template <int kBytes>
-__device__ __forceinline__ void copy_async2(uint32_t buf, int at, const void* from, int lane) {
-  const uint32_t to = buf + at + threadIdx.x * kBytes;
-  const char* src = static_cast<const char*>(from) + lane * kBytes;
-  copy_async<kBytes>(to, src);
-  copy_async<kBytes>(to + kMixThreads * kBytes, src + 32 * kBytes);
+// A warp's 256 fp32 values, in their order.
+__device__ __forceinline__ void copy_f32(uint32_t to, const float* from, int lane) {
+  to += (threadIdx.x & ~31) * 32 + lane * 16;
+  copy_async<16>(to, from + lane * 4);
+  copy_async<16>(to + 512, from + 128 + lane * 4);
 }
 
-__device__ __forceinline__ float4 from_buf16(uint32_t buf, int at) {
-  float4 x;
+__device__ __forceinline__ void from_buf_f32(uint32_t at, float2 (&x)[4]) {
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-               : "r"(buf + at + threadIdx.x * 16) : "memory");
-  return x;
+               : "=f"(x[0].x), "=f"(x[0].y), "=f"(x[1].x), "=f"(x[1].y)
+               : "r"(at + threadIdx.x * 32) : "memory");
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x[2].x), "=f"(x[2].y), "=f"(x[3].x), "=f"(x[3].y)
+               : "r"(at + threadIdx.x * 32 + 16) : "memory");
 }
 
-__device__ __forceinline__ void from_buf8(uint32_t buf, int at, float2 (&x)[4]) {
-  const float4 a = from_buf16(buf, at), b = from_buf16(buf, at + kMixThreads * 16);
-  x[0] = make_float2(a.x, a.y);
-  x[1] = make_float2(a.z, a.w);
-  x[2] = make_float2(b.x, b.y);
-  x[3] = make_float2(b.z, b.w);
-}
-
-__device__ __forceinline__ void from_buf8_bf16(uint32_t buf, int at, float2 (&x)[4]) {
+__device__ __forceinline__ void from_buf_bf16(uint32_t at, float2 (&x)[4]) {
   uint4 w;
-  const uint32_t p = buf + at + threadIdx.x * 8;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(p) : "memory");
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-               : "=r"(w.z), "=r"(w.w) : "r"(p + kMixThreads * 8) : "memory");
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+               : "r"(at + threadIdx.x * 16) : "memory");
   unpack8(w, x);
 }
 
-__device__ __forceinline__ uint32_t from_buf4(uint32_t buf, int at) {
-  uint32_t x;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(buf + at + threadIdx.x * 4) : "memory");
-  return x;
+__device__ __forceinline__ uint2 from_buf_codes(uint32_t at) {
+  uint2 w;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+               : "=r"(w.x), "=r"(w.y) : "r"(at + threadIdx.x * 8) : "memory");
+  return w;
 }
 
+// Waits until at most kPending of the lanes' groups are under way.
 template <int kPending>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+  __syncwarp();
 }
 
 __device__ __forceinline__ void copies_group() {
@@ -328,19 +315,23 @@ __device__ __forceinline__ void find_place(const P& a, uint32_t u, int warp, Mix
 __device__ __forceinline__ uint32_t fetch_moments(const MixSeg& s, const MixPlace& at,
                                                   uint32_t buf, int lane) {
   if (s.numel & kSegBf16)
-    copy_async2<8>(buf, kBufG, static_cast<const uint16_t*>(s.g) + at.i0, lane);
+    copy_async<16>(buf + kBufG + threadIdx.x * 16,
+                   static_cast<const uint16_t*>(s.g) + at.i0 + lane * 8);
   else
-    copy_async2<16>(buf, kBufG, static_cast<const float*>(s.g) + at.i0, lane);
-  copy_async2<4>(buf, kBufCodes, static_cast<uint8_t*>(s.m) + at.i0, lane);
-  copy_async2<4>(buf, kBufCodes + 1024, static_cast<uint8_t*>(s.v) + at.i0, lane);
+    copy_f32(buf + kBufG, static_cast<const float*>(s.g) + at.i0, lane);
+  const uint32_t codes = buf + kBufCodes + threadIdx.x * 8;
+  copy_async<8>(codes, static_cast<uint8_t*>(s.m) + at.i0 + lane * 8);
+  copy_async<8>(codes + kMixThreads * 8, static_cast<uint8_t*>(s.v) + at.i0 + lane * 8);
+  // (as two bytes joined here: one 16-bit load, first used by the next block,
+  // was measured 10 % slower over the whole kernel, on a 65,536 x 1024 table)
   return s.s[2ll * at.blk] | static_cast<uint32_t>(s.s[2ll * at.blk + 1]) << 8;
 }
 
 // Starts the copies that the weights need.
 __device__ __forceinline__ void fetch_weights(const MixSeg& s, const MixPlace& at, uint32_t buf,
                                               int lane) {
-  copy_async2<16>(buf, kBufP, s.p + at.i0, lane);
-  if (s.e) copy_async2<16>(buf, kBufE, s.e + at.i0, lane);
+  copy_f32(buf + kBufP, s.p + at.i0, lane);
+  if (s.e) copy_f32(buf + kBufE, s.e + at.i0, lane);
 }
 
 // New weights, averages and copies of a lane's 8 elements.
@@ -362,38 +353,40 @@ __device__ __forceinline__ void mixed_average(const P& a, const float2 (&p)[4], 
   for (int k = 0; k < 4; ++k) e[k] = __ffma2_rn(e[k], a.d, mul2(p[k], a.omd));
 }
 
-// Where a block's element j lies in the warp's part of a piece of the buffer, its elements
-// `size` bytes wide.
-__device__ __forceinline__ uint32_t in_buf(int j, int size) {
-  return (j >> 7) * kMixThreads * 4 * size + ((threadIdx.x & ~31) * 4 + (j & 127)) * size;
-}
-
 // The same for a block that is not full or not aligned: element by element,
 // zeros past the tensor's end.
 __device__ __forceinline__ void fetch_ragged(const MixSeg& s, const MixPlace& at,
                                              unsigned char* buf, int lane) {
-  __syncwarp();   // the lanes have read the block before
+  const bool g16 = (s.numel & kSegBf16) != 0;
+  float p[8], g[8], e[8];
+  uint32_t m[8], r[8];
 #pragma unroll
-  for (int j = lane; j < kA8Block; j += 32) {
+  for (int k = 0; k < 8; ++k) {   // everything is requested before the first use
+    const int j = k * 32 + lane;
     const bool in = j < at.left;
     const long long i = at.i0 + j;
-    if (s.numel & kSegBf16)
-      *reinterpret_cast<uint16_t*>(buf + kBufG + in_buf(j, 2)) =
-          in ? static_cast<const uint16_t*>(s.g)[i] : 0;
+    g[k] = !in ? 0.f : g16 ? bf16_at(s.g, i) : static_cast<const float*>(s.g)[i];
+    m[k] = in ? static_cast<uint8_t*>(s.m)[i] : 0u;
+    r[k] = in ? static_cast<uint8_t*>(s.v)[i] : 0u;
+    p[k] = in ? s.p[i] : 0.f;
+    e[k] = in && s.e ? s.e[i] : 0.f;
+  }
+  __syncwarp();   // the lanes have read the block before
+  const int first = threadIdx.x & ~31;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int j = k * 32 + lane, wide = first * 32 + j * 4;
+    if (g16)
+      *reinterpret_cast<uint16_t*>(buf + kBufG + first * 16 + j * 2) =
+          static_cast<uint16_t>(__float_as_uint(g[k]) >> 16);
     else
-      *reinterpret_cast<float*>(buf + kBufG + in_buf(j, 4)) =
-          in ? static_cast<const float*>(s.g)[i] : 0.f;
-    buf[kBufCodes + in_buf(j, 1)] = in ? static_cast<uint8_t*>(s.m)[i] : 0;
-    buf[kBufCodes + 1024 + in_buf(j, 1)] = in ? static_cast<uint8_t*>(s.v)[i] : 0;
-    *reinterpret_cast<float*>(buf + kBufP + in_buf(j, 4)) = in ? s.p[i] : 0.f;
-    if (s.e) *reinterpret_cast<float*>(buf + kBufE + in_buf(j, 4)) = in ? s.e[i] : 0.f;
+      *reinterpret_cast<float*>(buf + kBufG + wide) = g[k];
+    buf[kBufCodes + first * 8 + j] = static_cast<uint8_t>(m[k]);
+    buf[kBufCodes + kMixThreads * 8 + first * 8 + j] = static_cast<uint8_t>(r[k]);
+    *reinterpret_cast<float*>(buf + kBufP + wide) = p[k];
+    *reinterpret_cast<float*>(buf + kBufE + wide) = e[k];
   }
   __syncwarp();
-}
-
-// Element of a lane's k-th value.
-__device__ __forceinline__ int lane_element(int lane, int k) {
-  return lane * 4 + (k & 3) + 128 * (k >> 2);
 }
 
 // A block with an 8-bit state, its copies under way; next_moments and
@@ -403,29 +396,33 @@ __device__ __forceinline__ void mixed_block8(const P& a, const MixSeg& s, const 
                                              const MixPlace& at, uint32_t buf, uint32_t scale,
                                              int lane, const FM& next_moments,
                                              const FW& next_weights) {
-  const long long i = at.i0 + lane * 4;
+  const long long i = at.i0 + lane * 8;
   float2 m[4], nr[4];
   bool odd;
   {
     float2 g[4], r[4];
     copies_wait<1>();
-    if (kG16) from_buf8_bf16(buf, kBufG, g);
-    else from_buf8(buf, kBufG, g);
+    if (kG16) from_buf_bf16(buf + kBufG, g);
+    else from_buf_f32(buf + kBufG, g);
     const float mf = a8_factor(scale & 0xffu), rf = a8_factor(scale >> 8);
-    a8_decode_m4(from_buf4(buf, kBufCodes), mf, m);
-    a8_decode_m4(from_buf4(buf, kBufCodes + 512), mf, m + 2);
-    a8_decode_r4(from_buf4(buf, kBufCodes + 1024), rf, r);
-    a8_decode_r4(from_buf4(buf, kBufCodes + 1536), rf, r + 2);
+    const uint2 mw = from_buf_codes(buf + kBufCodes);
+    const uint2 rw = from_buf_codes(buf + kBufCodes + kMixThreads * 8);
+    a8_decode_m4(mw.x, mf, m);
+    a8_decode_m4(mw.y, mf, m + 2);
+    a8_decode_r4(rw.x, rf, r);
+    a8_decode_r4(rw.y, rf, r + 2);
+    if (!kG16) __syncwarp();   // before other lanes' pieces are replaced
     next_moments();
     odd = mixed_moments<true>(a, w, g, m, r, nr);
   }
   {
     float2 p[4], e[4];
     copies_wait<1>();
-    from_buf8(buf, kBufP, p);
-    if (s.e) from_buf8(buf, kBufE, e);
+    from_buf_f32(buf + kBufP, p);
+    if (s.e) from_buf_f32(buf + kBufE, e);
     mixed_weights(a, w, m, nr, p);
     if (s.e) mixed_average(a, p, e);
+    __syncwarp();   // before other lanes' pieces are replaced
     next_weights();
     if (at.full) {
       store8(s.p + i, p);
@@ -434,7 +431,7 @@ __device__ __forceinline__ void mixed_block8(const P& a, const MixSeg& s, const 
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int j = lane_element(lane, k);
+        const int j = lane * 8 + k;
         if (j >= at.left) continue;
         s.p[at.i0 + j] = ::muonb200::at(p, k);
         if (s.c) s.c[at.i0 + j] = __bfloat16_as_ushort(__float2bfloat16_rn(::muonb200::at(p, k)));
@@ -446,26 +443,25 @@ __device__ __forceinline__ void mixed_block8(const P& a, const MixSeg& s, const 
     // past the tensor's end nothing enters the block's largest
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (lane_element(lane, k) >= at.left) ::muonb200::at(m, k) = ::muonb200::at(nr, k) = 0.f;
+      if (lane * 8 + k >= at.left) ::muonb200::at(m, k) = ::muonb200::at(nr, k) = 0.f;
     odd = true;
   }
-  uint32_t word[8], m8[2], r8[2], mbyte, rbyte;
+  uint32_t x[8], m8[2], r8[2], mbyte, rbyte;
   if (kStochastic) {
-    // mix32(key of the block ^ element), its first step taken apart: the
-    // element's number (below 256) does not reach the upper half
+    // mix32(key of the block ^ element) but for its last step; of its first
+    // step, the element's number (below 256) does not reach the upper half
     uint32_t bkey = mix32(w.key ^ at.blk);
-    bkey = (bkey ^ (bkey >> 16)) ^ (lane * 4);
+    bkey = (bkey ^ (bkey >> 16)) ^ (lane * 8);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      uint32_t x = (bkey ^ ((k & 3) + 128 * (k >> 2))) * 0x57735285u;
-      x = (x ^ (x >> 15)) * 0x4746E6A3u;
-      word[k] = x ^ (x >> 16);
+      x[k] = (bkey ^ k) * 0x57735285u;
+      x[k] = (x[k] ^ (x[k] >> 15)) * 0x4746E6A3u;
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) word[k] = 0u;
+    for (int k = 0; k < 8; ++k) x[k] = 0u;
   }
-  a8_encode_block<kStochastic>(m, nr, word, odd, m8, r8, mbyte, rbyte);
+  a8_encode_block<kStochastic>(m, nr, x, odd, m8, r8, mbyte, rbyte);
   uint8_t* cm = static_cast<uint8_t*>(s.m);
   uint8_t* cr = static_cast<uint8_t*>(s.v);
   if (at.full) {
@@ -474,15 +470,19 @@ __device__ __forceinline__ void mixed_block8(const P& a, const MixSeg& s, const 
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int j = lane_element(lane, k);
+      const int j = lane * 8 + k;
       if (j >= at.left) continue;
       cm[at.i0 + j] = static_cast<uint8_t>(m8[k >> 2] >> (8 * (k & 3)));
       cr[at.i0 + j] = static_cast<uint8_t>(r8[k >> 2] >> (8 * (k & 3)));
     }
   }
   if (lane == 0) {
-    s.s[2ll * at.blk] = static_cast<uint8_t>(mbyte);
-    s.s[2ll * at.blk + 1] = static_cast<uint8_t>(rbyte);
+    if (at.full) {
+      reinterpret_cast<uint16_t*>(s.s)[at.blk] = static_cast<uint16_t>(mbyte | rbyte << 8);
+    } else {
+      s.s[2ll * at.blk] = static_cast<uint8_t>(mbyte);
+      s.s[2ll * at.blk + 1] = static_cast<uint8_t>(rbyte);
+    }
   }
 }
 
@@ -490,7 +490,7 @@ __device__ __forceinline__ void mixed_block8(const P& a, const MixSeg& s, const 
 template <bool kG16, class P>
 __device__ __forceinline__ void mixed_full32(const P& a, const MixSeg& s, const MixStep& w,
                                              const MixPlace& at, int lane) {
-  const long long i = at.i0 + lane * 4;
+  const long long i = at.i0 + lane * 8;
   float2 p[4], g[4], m[4], v[4], nr[4], e[4];
   load8(static_cast<const float*>(s.m) + i, m);
   load8(static_cast<const float*>(s.v) + i, v);
@@ -544,8 +544,8 @@ __device__ __forceinline__ void mixed_ragged32(const P& a, const MixSeg& s, cons
 
 // A thread block takes a unit of 4 blocks of 256 elements at a time, one warp
 // per block, so that everything about the tensor (table look-up, pointers) is
-// uniform over the thread block.  Full blocks of aligned tensors move in
-// 16-byte accesses (4 or 8 bytes of narrower types); ragged ends and unaligned
+// uniform over the thread block.  Full blocks of aligned tensors move 8
+// elements per lane at a time; ragged ends and unaligned
 // tensors go element by element.  Tensors with 8-bit states come first, in a
 // loop of their own (one loop for both forms spilled registers).
 template <bool kStochastic, int kSegs>
@@ -607,10 +607,12 @@ adamw_mixed_kernel(const __grid_constant__ MixParams<kSegs> a) {
                            (static_cast<uint32_t>(s.numel >> kSegPlace) & 0xffffu)));
   };
 
+  uint32_t set = 0xffffffffu;
   for (; u < a.units8; u += gridDim.x) {
     const MixPlace at = next;
     const MixSeg& s = a.seg[at.cur];
-    set_tensor(s);
+    if (at.cur != set) set_tensor(s);
+    set = at.cur;
     uint32_t scale_now = scale;
     next.full = false;
     if (u + gridDim.x < a.units8) find_place(a, u + gridDim.x, warp, next);
@@ -643,7 +645,8 @@ adamw_mixed_kernel(const __grid_constant__ MixParams<kSegs> a) {
   for (; u < n_units; u += gridDim.x) {
     find_place(a, u, warp, next);
     const MixSeg& s = a.seg[next.cur];
-    set_tensor(s);
+    if (next.cur != set) set_tensor(s);
+    set = next.cur;
     if (next.full) {
       if (s.numel & kSegBf16) mixed_full32<true>(a, s, w, next, lane);
       else mixed_full32<false>(a, s, w, next, lane);
@@ -692,7 +695,7 @@ adam8_write_kernel(const __grid_constant__ A8Params<kSegs> a) {
     if (left <= 0) continue;
     const bool vec = (s.numel & kSegVec) && left >= kA8Block;
     const bool b16 = (s.numel & kSegBf16) != 0;
-    const long long iv = i0 + lane * 4;
+    const long long iv = i0 + lane * 8;
     float2 m[4], r[4];
     if (vec) {
       if (b16) {
@@ -711,17 +714,17 @@ adam8_write_kernel(const __grid_constant__ A8Params<kSegs> a) {
         at(r, k) = !in ? 0.f : b16 ? bf16_at(s.v, i0 + j) : static_cast<float*>(s.v)[i0 + j];
       }
     }
-    uint32_t word[8], m8[2], r8[2], mbyte, rbyte;
+    uint32_t zero[8], m8[2], r8[2], mbyte, rbyte;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      word[k] = 0u;
+      zero[k] = 0u;
       // a second moment (or root) below zero is not one: NaN, like sqrt's
       float& x = at(r, k);
       if (b16) x = x < 0.f ? __uint_as_float(0x7fc00000u) : x;
       else x = __fsqrt_rn(x);
       x = -x;
     }
-    a8_encode_block<false>(m, r, word, true, m8, r8, mbyte, rbyte);
+    a8_encode_block<false>(m, r, zero, true, m8, r8, mbyte, rbyte);
     if (vec) {
       store8_codes(s.m8 + iv, m8);
       store8_codes(s.r8 + iv, r8);
@@ -761,7 +764,7 @@ adam8_read_kernel(const __grid_constant__ A8Params<kSegs> a) {
     if (left <= 0) continue;
     const bool vec = (s.numel & kSegVec) && left >= kA8Block;
     const bool b16 = (s.numel & kSegBf16) != 0;
-    const long long iv = i0 + lane * 4;
+    const long long iv = i0 + lane * 8;
     const float mf = a8_factor(s.s[2ll * blk]), rf = a8_factor(s.s[2ll * blk + 1]);
     float2 m[4], r[4];
     if (vec) {

@@ -98,9 +98,9 @@ muon_status_t mixed_launch(const adamw_mixed_tensor_t* x, int first, int n,
       const uintptr_t wide = bits(t.param) | bits(t.ema);
       const bool g16 = t.grad_dtype == MUON_BF16;
       const uintptr_t codes = bits(t.exp_avg) | bits(t.exp_avg_sq);
-      const bool vec = ((wide | (eight ? 0 : codes) | (g16 ? 0 : bits(t.grad))) & 15u) == 0 &&
-                       ((bits(t.copy_bf16) | (g16 ? bits(t.grad) : 0)) & 7u) == 0 &&
-                       (codes & 3u) == 0;
+      const uintptr_t halves = bits(t.copy_bf16) | (g16 ? bits(t.grad) : 0);
+      const bool vec = ((wide | (eight ? 0 : codes) | (g16 ? 0 : bits(t.grad))) & 31u) == 0 &&
+                       (halves & 15u) == 0 && (codes & 7u) == 0 && (bits(t.scale) & 1u) == 0;
       a.seg[k] = MixSeg{t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.scale, t.ema, t.copy_bf16,
                         flagged(t.numel, g16, vec) |
                             static_cast<unsigned long long>(i) << kSegPlace,
@@ -148,8 +148,8 @@ muon_status_t adam8_launch(const adam8_tensor_t* x, int n, int32_t dtype, bool w
   for (int i = 0; i < n; ++i) {
     const adam8_tensor_t& t = x[i];
     const bool vec =
-        ((bits(t.exp_avg) | bits(t.second)) & (dtype == MUON_BF16 ? 7u : 15u)) == 0 &&
-        ((bits(t.exp_avg8) | bits(t.root8)) & 3u) == 0;
+        ((bits(t.exp_avg) | bits(t.second)) & (dtype == MUON_BF16 ? 15u : 31u)) == 0 &&
+        ((bits(t.exp_avg8) | bits(t.root8)) & 7u) == 0;
     a.seg[i] = A8Seg{t.exp_avg8, t.root8, t.scale, t.exp_avg, t.second,
                      flagged(t.numel, dtype == MUON_BF16, vec)};
     a.ubeg[i] = units;
