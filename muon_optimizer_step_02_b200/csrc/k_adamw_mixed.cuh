@@ -26,6 +26,7 @@
 #include <cuda_bf16.h>
 
 #include "k_adam8.cuh"
+#include "sm100_ptx.cuh"
 
 namespace muonb200 {
 
@@ -562,6 +563,8 @@ adamw_mixed_kernel(const __grid_constant__ MixParams<kSegs> a) {
   uint32_t scale = 0;
   uint32_t u = blockIdx.x;
   if (u < a.units8) find_place(a, u, warp, next);
+  grid_launch_dependents();
+  grid_dependency_wait();   // nothing above touches memory
   if (next.full) scale = fetch_moments(a.seg[next.cur], next, buf, lane);
   copies_group();
   if (next.full) fetch_weights(a.seg[next.cur], next, buf, lane);
@@ -683,6 +686,8 @@ adam8_write_kernel(const __grid_constant__ A8Params<kSegs> a) {
   const int lane = threadIdx.x & 31, warp = warp_number();
   const uint32_t n_units = a.ubeg[a.n_seg];
   uint32_t cur = 0, end = 0;
+  grid_launch_dependents();
+  grid_dependency_wait();
   for (uint32_t u = blockIdx.x; u < n_units; u += gridDim.x) {
     if (u >= end) {
       cur = find_seg(a.ubeg, a.n_seg, u);
@@ -752,6 +757,8 @@ adam8_read_kernel(const __grid_constant__ A8Params<kSegs> a) {
   const int lane = threadIdx.x & 31, warp = warp_number();
   const uint32_t n_units = a.ubeg[a.n_seg];
   uint32_t cur = 0, end = 0;
+  grid_launch_dependents();
+  grid_dependency_wait();
   for (uint32_t u = blockIdx.x; u < n_units; u += gridDim.x) {
     if (u >= end) {
       cur = find_seg(a.ubeg, a.n_seg, u);

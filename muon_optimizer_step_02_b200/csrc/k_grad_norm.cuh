@@ -114,6 +114,8 @@ grad_norm_kernel(const __grid_constant__ NormParams<kSegs> a) {
   const uint32_t n_units = a.ubeg[a.n_seg];
   uint32_t cur = 0, end = 0;
   double sum[4] = {0.0, 0.0, 0.0, 0.0};
+  grid_launch_dependents();
+  grid_dependency_wait();
   for (uint32_t u = blockIdx.x; u < n_units; u += gridDim.x) {
     if (u >= end) {
       cur = find_seg(a.ubeg, a.n_seg, u);

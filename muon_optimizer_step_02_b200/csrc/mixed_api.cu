@@ -48,12 +48,23 @@ inline float2 twice(double x) {
   return make_float2(static_cast<float>(x), static_cast<float>(x));
 }
 
+// Launched as a programmatic dependent of whatever runs before it on the
+// stream: its thread blocks may be set up while that ends (the kernels wait for
+// its completion before they touch memory).
 template <class P>
 muon_status_t launch(void (*kernel)(P), const P& params, unsigned grid, int threads,
                      cudaStream_t st) {
   void* args[] = {const_cast<P*>(&params)};
-  if (cudaLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(grid), dim3(threads),
-                       args, 0, st) != cudaSuccess) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kernel), args) != cudaSuccess) {
     cudaGetLastError();
     return MUON_ERR_CUDA;
   }

@@ -579,6 +579,137 @@ def test_writing_what_is_no_moment():
         assert M[700].item() == 0 and V[700].item() == 0 and bool((V[512:700] == 1).all())
 
 
+# ---- what runs before and after, on the stream and in graphs --------------------
+
+def _chain(B, c, h):
+    """norm -> clipped step -> read-back of one case, as bound calls."""
+    import torch
+    out = torch.zeros(2, device="cuda")
+    step = torch.zeros(2, dtype=torch.int32, device="cuda")
+    m = [torch.zeros(n, dtype=torch.bfloat16, device="cuda") for n in c.sizes]
+    r = [torch.zeros(n, dtype=torch.bfloat16, device="cuda") for n in c.sizes]
+    calls = (B.grad_norm_bind(c.G, 0.01, out, B.grad_norm_workspace()),
+             B.adamw_mixed_bind(c.P, c.G, c.S, h, c.E, c.C, DECAY, step_dev=step,
+                                grad_scale=out[1:], rounding="stochastic", seed=4),
+             B.adam8_read_bind(c.S, m, r))
+    return calls, [out, step, *m, *r, *c.arrays()]
+
+
+@pytest.mark.parametrize("n", [1000, 3 << 20])
+def test_calls_see_what_ran_before_them(n):
+    """The kernels may be set up while what precedes them still runs: each of a
+    copy, a fill, a library kernel, a plain kernel of another stream and a
+    call of the same kind, eagerly and in a graph, is seen whole; and what
+    follows sees the calls' results."""
+    import torch
+    from muon_optimizer_step_02_b200 import binding as B
+    h = hyper(beta2=0.99)
+    sizes = [n, 77]
+    ref, eager, graphed = (Case(sizes, FORMATS["8"], seed=2) for _ in range(3))
+    src = [torch.from_numpy(wl.adamw_grad(k, i, 7, 2, wid=300)).cuda() for i, k in enumerate(sizes)]
+    big = torch.randn(2048, 2048, device="cuda")
+
+    def program(c, calls, after, wait):
+        side = torch.cuda.Stream()
+        norm, step, read = calls
+
+        def passes():
+            for g, x in zip(c.G, src):
+                g.copy_(x)                       # a copy, then the norm
+            wait()
+            norm()
+            wait()
+            step()
+            wait()
+            c.G[0].fill_(0.25)                   # a fill, then the norm
+            wait()
+            norm()
+            wait()
+            step()
+            wait()
+            y = big @ big                        # a library's product, then the step
+            c.G[1].copy_(y[0, :77] * 1e-3)
+            wait()
+            step()
+            wait()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):        # another stream's work, joined
+                c.G[0].mul_(0.5)
+                c.G[1].add_(1e-3)
+            torch.cuda.current_stream().wait_stream(side)
+            wait()
+            norm()
+            wait()
+            step()
+            wait()
+            step()
+            wait()
+            read()
+            wait()
+            after[0].copy_(c.P[0])               # a kernel that reads the results
+            after[1].copy_(c.G[0] * 2)
+        return passes
+
+    results = []
+    for c, how in ((ref, "waits"), (eager, "eager"), (graphed, "graph")):
+        calls, arrays = _chain(B, c, h)
+        after = [torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")]
+        run = program(c, calls, after, torch.cuda.synchronize if how == "waits" else lambda: None)
+        if how == "graph":
+            run()                                # workspaces of the product, once
+            torch.cuda.synchronize()
+            fresh = Case(sizes, FORMATS["8"], seed=2)
+            for x, y in zip(c.arrays(), fresh.arrays()):
+                x.copy_(y)
+            arrays[1].zero_()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                run()
+            graph.replay()
+            torch.cuda.synchronize()
+            del graph
+        else:
+            run()
+            torch.cuda.synchronize()
+        results.append(arrays + after)
+    for x, y, z in zip(*results):
+        assert torch.equal(x, y) and torch.equal(x, z)
+
+
+def test_interleaved_with_the_other_optimizer_calls():
+    """Between Muon steps (whose tensor-core kernel is itself a dependent
+    launch), with 0 and 5 Newton-Schulz steps, and EMA passes: bit for bit what
+    the same calls give with waits between them."""
+    import torch
+    from gpu_harness import GpuMuon
+    from muon_optimizer_step_02_b200 import binding as B
+    h, ah = wl.Hyper(momentum=0.95, lr=0.02, weight_decay=0.1), hyper()
+    results = []
+    for wait in (torch.cuda.synchronize, lambda: None):
+        kept = []
+        for coeffs in ([wl.FIXED_QUINTIC] * 5, []):
+            w = wl.custom([(512, 256), (128, 384)], h, coeffs, name="interleaved")
+            mu = GpuMuon(w, with_out=False)
+            mg = mu.grads(0)
+            c = Case([4099, 512], FORMATS["mixed"])
+            calls, arrays = _chain(B, Case([3000], FORMATS["8"]), ah)
+            em = [x.clone().view(-1) for x in mu.W]
+            adam = B.adamw_mixed_bind(c.P, c.G, c.S, ah, c.E, c.C, DECAY)
+            for t in range(1, 4):
+                for call in (calls[0], lambda: mu.step(mg), lambda: adam(step_now=t), calls[1],
+                             lambda: B.ema_update_batched(em, [x.view(-1) for x in mu.W], DECAY),
+                             calls[2], lambda: mu.step(mg), calls[1]):
+                    call()
+                    wait()
+            torch.cuda.synchronize()
+            assert mu.plan.last_error() == 0
+            kept += [*mu.W, *mu.M, *em, *c.arrays(), *arrays]
+            mu.plan.close()
+        results.append(kept)
+    for x, y in zip(*results):
+        assert torch.equal(x, y)
+
+
 # ---- refusals that need device tensors ----------------------------------------
 
 def test_binding_refusals():
