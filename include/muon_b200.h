@@ -248,7 +248,7 @@ typedef enum { MUON_ROUND_NEAREST = 0, MUON_ROUND_STOCHASTIC = 1 } muon_round_t;
  * beta1, beta2 in [0, 1); eps >= 0.  seed gives the random bits of
  * stochastic rounding, with the step number, the tensor's place in the call
  * and the element's place in the tensor: the same call on the same inputs
- * gives the same bits. */
+ * gives the same bits, and calls on different tensors want different seeds. */
 typedef struct {
   double lr;
   double beta1;
@@ -275,8 +275,9 @@ typedef struct {
  *  ema         fp32, updated in place, or NULL.
  *  copy_bf16   receives the new parameters rounded to bf16, or NULL.
  *  lr_scale, wd_scale  multiply lr and weight_decay for this tensor.
- * fp32 arrays need 4-byte alignment, bf16 arrays 2-byte; tensors whose
- * arrays are 16-byte aligned (codes: 8-byte) take the vectorised path.
+ * fp32 arrays need 4-byte alignment, bf16 arrays 2-byte; tensors whose fp32
+ * arrays are 32-byte aligned, bf16 arrays 16-byte, codes 8-byte and scale
+ * 2-byte take the vectorised path.
  * Arrays must not overlap, within a tensor or between tensors. */
 typedef struct {
   float *param;
@@ -313,7 +314,10 @@ typedef struct {
  * not 0.  Up to 400 tensors per
  * launch; at most 2^39 elements per call (MUON_ERR_UNSUPPORTED).
  * Asynchronous on `stream`; argument errors are returned before anything is
- * enqueued.  Deterministic. */
+ * enqueued.  Deterministic.  The kernels of this call and of the three below
+ * are launched as programmatic dependents: they may be set up while what
+ * precedes them on the stream ends, and wait for its completion before they
+ * read or write memory. */
 muon_status_t adamw_mixed_batched(const adamw_mixed_tensor_t *tensors, int32_t n_tensors,
                                   const adamw_mixed_hyper_t *hyper, int32_t step,
                                   int32_t *step_dev, const float *lr_dev,

@@ -496,10 +496,16 @@ def adamw_ema_launches(n_tensors: int, with_step_dev: bool = False) -> int:
 
 # ---- AdamW with 32-bit or 8-bit moments --------------------------------------
 
-def _dense(t, dtypes, numel, what, device=None):
+def _dense(t, dtypes, numel, what, device=None, i=None):
     """Checks a contiguous CUDA tensor of one of `dtypes` with `numel` elements
-    (None: any number) on `device` (None: any); returns it."""
+    (None: any number) on `device` (None: any); returns it.  what, i: its name
+    and place in a list."""
     import torch
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and \
+            t.is_contiguous() and (numel is None or t.numel() == numel) and \
+            (device is None or t.get_device() == device.index):
+        return t
+    what = _name(what, i)
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
     if t.dtype not in dtypes:
@@ -508,52 +514,63 @@ def _dense(t, dtypes, numel, what, device=None):
         raise ValueError(f"{what} must be contiguous")
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{what} has {t.numel()} elements, expected {numel}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{what} is on {t.device}, expected {device}")
-    return t
+    raise ValueError(f"{what} is on {t.device}, expected {device}")
+
+
+def _name(what, i):
+    return what if i is None else what.format(i)
 
 
 def _check_overlap(written, read):
     """Raises if a written array shares memory with any other array of the
-    call (the same tensor passed twice among them).  Entries: (tensor, name)."""
-    spans = [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), w, name)
-             for w, group in ((True, written), (False, read))
-             for t, name in group if t is not None and t.numel() > 0]
+    call (the same tensor passed twice among them).  Entries: (tensor, name,
+    place in a list or None)."""
+    spans = []
+    for w, group in ((True, written), (False, read)):
+        for x in group:
+            t = x[0]
+            if t is not None and (k := t.numel()):
+                p = t.data_ptr()
+                spans.append((p, p + k * t.element_size(), w, x))
     spans.sort(key=lambda x: x[:2])
-    end, end_w, name, name_w = 0, 0, "", ""   # furthest ends so far: any span, a written one
-    for b, e, w, what in spans:
+    end = end_w = 0        # furthest ends so far, of any array and of a written one,
+    far = far_w = None     # and whose they are
+    for b, e, w, x in spans:
         if b < end_w or (w and b < end):
-            raise ValueError(f"{what} overlaps {name_w if b < end_w else name}")
+            raise ValueError(f"{_name(*x[1:])} overlaps "
+                             f"{_name(*(far_w if b < end_w else far)[1:])}")
         if e > end:
-            end, name = e, what
+            end, far = e, x
         if w and e > end_w:
-            end_w, name_w = e, what
+            end_w, far_w = e, x
 
 
-def _on_device(fn, device):
-    """call(*args, stream=None): fn(*args, stream handle) with `device` current,
-    on `stream` or the device's current stream."""
+def _bound(fn, what, device, keep):
+    """run(args, stream=None): fn(*args, stream handle) with `device` current, on
+    `stream` or the device's current stream; raises on an error status.  keep:
+    what has to live as long as the callable."""
     import torch
-    if device is None:
-        return lambda *args, stream=None: fn(*args, _stream_handle(stream))
-    index, current_device = device.index, torch.cuda.current_device
+    index = None if device is None else device.index
+    current_device = torch.cuda.current_device
     # the current stream's handle without an object around it (3 us a call)
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
-    def call(*args, stream=None):
-        if stream is None:
-            handle = raw(index)
-        else:
-            if getattr(stream, "device", device) != device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-            handle = _stream_handle(stream)
-        if current_device() == index:
-            fn(*args, handle)
-        else:
-            with torch.cuda.device(index):
-                fn(*args, handle)
-    return call
+    def elsewhere(args, stream):
+        if device is None:
+            return fn(*args, _stream_handle(stream))
+        if stream is not None and getattr(stream, "device", device) != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        with torch.cuda.device(index):
+            return fn(*args, raw(index) if stream is None else _stream_handle(stream))
+
+    def run(args, stream=None):
+        _ = keep
+        status = fn(*args, raw(index)) if stream is None and index == current_device() \
+            else elsewhere(args, stream)
+        if status != MUON_OK:
+            raise MuonError(status, what)
+    return run
 
 
 class Adam8State:
@@ -596,24 +613,19 @@ def grad_norm_bind(grads: Sequence, max_norm: float, out, workspace):
     n = len(grads)
     dev = _dense(out, (torch.float32,), 2, "out").device
     _dense(workspace, (torch.uint8,), None, "workspace", dev)
-    arr = (grad_tensor_t * max(n, 1))()
+    arr, kinds = (grad_tensor_t * max(n, 1))(), (torch.float32, torch.bfloat16)
     for i, g in enumerate(grads):
-        _dense(g, (torch.float32, torch.bfloat16), None, f"grads[{i}]", dev)
+        _dense(g, kinds, None, "grads[{}]", dev, i)
         arr[i] = grad_tensor_t(g.data_ptr(), g.numel(),
                                MUON_BF16 if g.dtype == torch.bfloat16 else MUON_F32)
-    _check_overlap([(out, "out"), (workspace, "workspace")],
-                   [(g, f"grads[{i}]") for i, g in enumerate(grads)])
-    fn = lib().grad_norm_batched
-    keep = (arr, list(grads), out, workspace)
-    limit, ws, ws_n, po = float(max_norm), workspace.data_ptr(), workspace.numel(), out.data_ptr()
-
-    def call(stream):
-        _ = keep
-        _check(fn(arr, n, limit, ws, ws_n, po, stream), "grad_norm_batched")
-    on_device = _on_device(call, dev)
+    _check_overlap([(out, "out", None), (workspace, "workspace", None)],
+                   [(g, "grads[{}]", i) for i, g in enumerate(grads)])
+    args = (arr, n, float(max_norm), workspace.data_ptr(), workspace.numel(), out.data_ptr())
+    call = _bound(lib().grad_norm_batched, "grad_norm_batched", dev,
+                  (arr, list(grads), out, workspace))
 
     def run(stream=None):
-        on_device(stream=stream)
+        call(args, stream)
     return run
 
 
@@ -639,69 +651,76 @@ def adamw_mixed_bind(params: Sequence, grads: Sequence, states: Sequence, hyper,
     before the first step) the device counts the steps; otherwise `step`, or
     run's `step_now`.  lr_dev: one fp32 read in place of hyper.lr.
     grad_scale: one fp32 that multiplies the gradients, such as out[1:] of
-    grad_norm_bind; a value that is not finite skips the step.  rounding and
-    seed: how new moments go to 8 bits."""
+    grad_norm_bind; a value that is not finite skips the step.  rounding
+    ("nearest" or "stochastic") and seed: how new moments go to 8 bits; calls
+    on different tensors want different seeds."""
     import torch
-    f32, u8 = (torch.float32,), (torch.uint8,)
+    f32 = (torch.float32,)
     n = len(params)
     emas = [None] * n if emas is None else list(emas)
     copies = [None] * n if copies is None else list(copies)
-    lr_scales = [1.0] * n if lr_scales is None else list(lr_scales)
-    wd_scales = [1.0] * n if wd_scales is None else list(wd_scales)
+    lr_scales = [1.0] * n if lr_scales is None else [float(x) for x in lr_scales]
+    wd_scales = [1.0] * n if wd_scales is None else [float(x) for x in wd_scales]
     if not (len(grads) == len(states) == len(emas) == len(copies) == len(lr_scales)
             == len(wd_scales) == n):
         raise ValueError("one grad, state, ema, copy and scale entry per param")
+    if int(step) > 0x7FFFFFFF:
+        raise ValueError(f"step {step} does not fit 32 bits")
     if rounding not in _ROUNDINGS:
         raise ValueError(f"rounding must be one of {sorted(_ROUNDINGS)}, got {rounding!r}")
     dev = next((t.device for t in (*params, step_dev) if isinstance(t, torch.Tensor)), None)
     written, read = [], []
     arr = (adamw_mixed_tensor_t * max(n, 1))()
+    b16, either, u8 = (torch.bfloat16,), (torch.float32, torch.bfloat16), (torch.uint8,)
     for i in range(n):
-        p = _dense(params[i], f32, None, f"params[{i}]", dev)
+        p = _dense(params[i], f32, None, "params[{}]", dev, i)
         k = p.numel()
-        g = _dense(grads[i], (torch.float32, torch.bfloat16), k, f"grads[{i}]", dev)
+        g = _dense(grads[i], either, k, "grads[{}]", dev, i)
         if isinstance(states[i], Adam8State):
             m, v, s = states[i].exp_avg, states[i].root, states[i].scale
-            _dense(m, u8, k, f"states[{i}].exp_avg", dev)
+            _dense(m, u8, k, "states[{}].exp_avg", dev, i)
         else:
             (m, v), s = states[i], None
-            _dense(m, f32, k, f"states[{i}][0]", dev)
-            _dense(v, f32, k, f"states[{i}][1]", dev)
+            _dense(m, f32, k, "states[{}][0]", dev, i)
+            _dense(v, f32, k, "states[{}][1]", dev, i)
         e, c = emas[i], copies[i]
         if e is not None:
-            _dense(e, f32, k, f"emas[{i}]", dev)
+            _dense(e, f32, k, "emas[{}]", dev, i)
         if c is not None:
-            _dense(c, (torch.bfloat16,), k, f"copies[{i}]", dev)
-        ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
-        arr[i] = adamw_mixed_tensor_t(ptr(p), ptr(g), ptr(m), ptr(v), ptr(s), ptr(e), ptr(c), k,
-                                      float(lr_scales[i]), float(wd_scales[i]),
-                                      MUON_BF16 if g.dtype == torch.bfloat16 else MUON_F32)
-        written += [(p, f"params[{i}]"), (m, f"first moment {i}"), (v, f"second moment {i}"),
-                    (s, f"scale {i}"), (e, f"emas[{i}]"), (c, f"copies[{i}]")]
-        read += [(g, f"grads[{i}]")]
+            _dense(c, b16, k, "copies[{}]", dev, i)
+        arr[i] = adamw_mixed_tensor_t(
+            p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(),
+            None if s is None else s.data_ptr(), None if e is None else e.data_ptr(),
+            None if c is None else c.data_ptr(), k, lr_scales[i], wd_scales[i],
+            MUON_BF16 if g.dtype == torch.bfloat16 else MUON_F32)
+        written += ((p, "params[{}]", i), (m, "states[{}]'s first moment", i),
+                    (v, "states[{}]'s second moment", i), (s, "states[{}]'s scale", i),
+                    (e, "emas[{}]", i), (c, "copies[{}]", i))
+        read.append((g, "grads[{}]", i))
     for t, dt, k, what in ((step_dev, torch.int32, 2, "step_dev"),
                            (lr_dev, torch.float32, 1, "lr_dev"),
                            (grad_scale, torch.float32, 1, "grad_scale")):
         if t is not None:
             _dense(t, (dt,), k, what, dev)
-            (written if what == "step_dev" else read).append((t, what))
+            (written if what == "step_dev" else read).append((t, what, None))
     _check_overlap(written, read)
     hp = adamw_mixed_hyper_t(float(hyper.lr), float(hyper.beta1), float(hyper.beta2),
                              float(hyper.eps), float(hyper.weight_decay), float(ema_decay),
                              int(seed) & 0xFFFFFFFFFFFFFFFF, _ROUNDINGS[rounding])
     hp_ref = ctypes.byref(hp)
     dptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
-    sp, lp, cp = dptr(step_dev), dptr(lr_dev), dptr(grad_scale)
-    fn = lib().adamw_mixed_batched
-    keep = (arr, hp, written, read)
-
-    def call(t, stream):
-        _ = keep
-        _check(fn(arr, n, hp_ref, t, sp, lp, cp, stream), "adamw_mixed_batched")
-    on_device = _on_device(call, dev)
+    pointers = (dptr(step_dev), dptr(lr_dev), dptr(grad_scale))
+    args = (arr, n, hp_ref, int(step), *pointers)
+    call = _bound(lib().adamw_mixed_batched, "adamw_mixed_batched", dev,
+                  (arr, hp, written, read))
 
     def run(step_now: Optional[int] = None, stream=None):
-        on_device(int(step if step_now is None else step_now), stream=stream)
+        if step_now is None:
+            call(args, stream)
+        elif int(step_now) > 0x7FFFFFFF:
+            raise ValueError(f"step {step_now} does not fit 32 bits")
+        else:
+            call((arr, n, hp_ref, int(step_now), *pointers), stream)
     return run
 
 
@@ -720,29 +739,24 @@ def _adam8_bind(states, exp_avgs, seconds, write: bool):
     if dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"plain moments must be torch.float32 or torch.bfloat16, got {dtype}")
     dev = states[0].exp_avg.device if n else None
-    coded, plain = [], []
+    coded, plain, u8, kind = [], [], (torch.uint8,), (dtype,)
     for i, (s, m, v) in enumerate(zip(states, exp_avgs, seconds)):
-        _dense(s.exp_avg, (torch.uint8,), s.numel, f"states[{i}].exp_avg", dev)
-        _dense(m, (dtype,), s.numel, f"exp_avgs[{i}]", dev)
-        _dense(v, (dtype,), s.numel, f"seconds[{i}]", dev)
+        _dense(s.exp_avg, u8, s.numel, "states[{}].exp_avg", dev, i)
+        _dense(m, kind, s.numel, "exp_avgs[{}]", dev, i)
+        _dense(v, kind, s.numel, "seconds[{}]", dev, i)
         arr[i] = adam8_tensor_t(s.exp_avg.data_ptr(), s.root.data_ptr(), s.scale.data_ptr(),
                                 m.data_ptr(), v.data_ptr(), s.numel)
-        coded += [(s.exp_avg, f"states[{i}].exp_avg"), (s.root, f"states[{i}].root"),
-                  (s.scale, f"states[{i}].scale")]
-        plain += [(m, f"exp_avgs[{i}]"), (v, f"seconds[{i}]")]
+        coded += ((s.exp_avg, "states[{}].exp_avg", i), (s.root, "states[{}].root", i),
+                  (s.scale, "states[{}].scale", i))
+        plain += ((m, "exp_avgs[{}]", i), (v, "seconds[{}]", i))
     _check_overlap(coded if write else plain, plain if write else coded)
-    fn = lib().adam8_write_batched if write else lib().adam8_read_batched
     what = "adam8_write_batched" if write else "adam8_read_batched"
-    dt = MUON_BF16 if dtype == torch.bfloat16 else MUON_F32
-    keep = (arr, list(states), list(exp_avgs), list(seconds))
-
-    def call(stream):
-        _ = keep
-        _check(fn(arr, n, dt, stream), what)
-    on_device = _on_device(call, dev)
+    args = (arr, n, MUON_BF16 if dtype == torch.bfloat16 else MUON_F32)
+    call = _bound(getattr(lib(), what), what, dev,
+                  (arr, list(states), list(exp_avgs), list(seconds)))
 
     def run(stream=None):
-        on_device(stream=stream)
+        call(args, stream)
     return run
 
 

@@ -16,6 +16,18 @@
 // A coefficient that is not finite (some gradient was not) skips the step:
 // nothing is written and the device's step count stays.
 //
+// Bytes per element: parameter 8, gradient 4 or 2, moments 16 or 4 (and 4 per
+// 256), average 8, copy 2.  Measured on a 65,536 x 1024 table with bf16
+// gradients and a copy: 313 us with 32-bit moments (28 bytes: 6.0 TB/s, 0.92 of
+// the measured copy bandwidth), 174-190 us with 8-bit ones, rounded
+// stochastically (16 bytes: 5.6-6.2 TB/s, 0.86-0.94), 195-200 us when it runs on
+// end, for then the GPU's power limit lowers the clock.  The 8-bit step is
+// bound by memory and by issue about equally (565 instructions per warp and
+// block of 256, an issue slot in use in 7 of 10 cycles), so it is built to
+// issue little: two elements to a register pair wherever the arithmetic has a
+// two-value form, addresses and tensor look-up in uniform registers, the next
+// block's data on their way through shared memory while one is computed.
+//
 // Source: PR #1893 "Record: L_ParallelResiduals_UNetSkips_DepthRecur_Muon_
 // 1.0901", table "Architecture and training stack", rows "Optimizer" (AdamW
 // on embeddings/scalars) and "EMA"; the page gives no setting and no state
@@ -31,7 +43,8 @@
 namespace muonb200 {
 
 constexpr int kMixThreads = 128;      // 4 warps: a unit of 4 blocks of 256 elements
-constexpr int kMixResident = 6;       // thread blocks per SM (78 registers)
+constexpr int kMixResident = 6;       // thread blocks per SM (76 registers); 8-bit table above with
+                                      // 5, 6, 7: 179, 174, 194 us
 constexpr int kMixUnit = kMixThreads * 8;
 constexpr int kMixMaxSegs = 400;      // 400 x 76 bytes of kernel parameters (limit 32,764)
 
@@ -162,6 +175,14 @@ __device__ __forceinline__ float2 minus_root2(float2 minus_v) {
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(-minus_v.y));
   const float2 s = mul2(minus_v, y);
   return __ffma2_rn(__ffma2_rn(s, s, minus_v), mul2(y, make_float2(0.5f, 0.5f)), s);
+}
+
+// Minus the square roots of any two values, rounded to the nearest.
+__device__ __forceinline__ float2 minus_root_any(float2 v) {
+  float2 x = minus_root2(make_float2(-v.x, -v.y));
+  if (!(v.x >= 0x1p-98f && v.x < INFINITY)) x.x = -__fsqrt_rn(v.x);
+  if (!(v.y >= 0x1p-98f && v.y < INFINITY)) x.y = -__fsqrt_rn(v.y);
+  return x;
 }
 
 // 1 / x to one unit in the last place; x below the normal range counts as 0.
@@ -719,16 +740,21 @@ adam8_write_kernel(const __grid_constant__ A8Params<kSegs> a) {
         at(r, k) = !in ? 0.f : b16 ? bf16_at(s.v, i0 + j) : static_cast<float*>(s.v)[i0 + j];
       }
     }
+    // r: the roots with a minus sign
+    if (b16) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        // a root below zero is not one: NaN, like a negative number's root
+        float& x = at(r, k);
+        x = x < 0.f ? __uint_as_float(0x7fc00000u) : -x;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r[k] = minus_root_any(r[k]);
+    }
     uint32_t zero[8], m8[2], r8[2], mbyte, rbyte;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      zero[k] = 0u;
-      // a second moment (or root) below zero is not one: NaN, like sqrt's
-      float& x = at(r, k);
-      if (b16) x = x < 0.f ? __uint_as_float(0x7fc00000u) : x;
-      else x = __fsqrt_rn(x);
-      x = -x;
-    }
+    for (int k = 0; k < 8; ++k) zero[k] = 0u;
     a8_encode_block<false>(m, r, zero, true, m8, r8, mbyte, rbyte);
     if (vec) {
       store8_codes(s.m8 + iv, m8);

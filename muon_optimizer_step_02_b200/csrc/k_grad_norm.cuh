@@ -11,6 +11,14 @@
 // every run.  Tensors past one launch's table go into further launches, each
 // adding its sum to the workspace's carry.
 //
+// Bound by memory: 4 or 2 bytes per element.  Each thread block keeps four
+// chunks of 2,048 elements in flight (two: 77 us, eight: 60 us on the first
+// figure below; small gradients come in more even shares with fewer).  The
+// conversions to 64 bits fill 60 % of their pipe at that rate and the GPU's
+// power limit lowers the clock when the call runs on end.  184 M bf16
+// gradients: 60 us (6.1 TB/s, 0.94 of the measured copy bandwidth), 69 us on
+// end; 67 M fp32: 43 us (6.2 TB/s).
+//
 // Context: PR #1893 "Record: L_ParallelResiduals_UNetSkips_DepthRecur_Muon_
 // 1.0901", table "Architecture and training stack"; the pages print no
 // clipping rule, the formula is the usual one of clipping by a global norm.

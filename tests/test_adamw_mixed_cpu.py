@@ -149,12 +149,12 @@ def test_overlap_check():
 
     def bad(written, read):
         with pytest.raises(ValueError, match="overlaps"):
-            B._check_overlap([(t, f"w{i}") for i, t in enumerate(written)],
-                             [(t, f"r{i}") for i, t in enumerate(read)])
+            B._check_overlap([(t, "w{}", i) for i, t in enumerate(written)],
+                             [(t, "r{}", i) for i, t in enumerate(read)])
 
     def good(written, read):
-        B._check_overlap([(t, f"w{i}") for i, t in enumerate(written)],
-                         [(t, f"r{i}") for i, t in enumerate(read)])
+        B._check_overlap([(t, "w{}", i) for i, t in enumerate(written)],
+                         [(t, "r{}", i) for i, t in enumerate(read)])
     bad([a, a], [])
     bad([a[:5]], [a[4:]])
     bad([a[2:3]], [a])

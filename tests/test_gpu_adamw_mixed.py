@@ -264,6 +264,41 @@ def test_many_tensors_take_several_launches():
     check(c, before, h, 4, rounding="stochastic", seed=9)
 
 
+def test_a_call_without_elements_counts_its_step():
+    import torch
+    from muon_optimizer_step_02_b200 import binding as B
+    step = torch.zeros(2, dtype=torch.int32, device="cuda")
+    empty = torch.zeros(0, device="cuda")
+    runs = [B.adamw_mixed_bind([], [], [], hyper(), step_dev=step),
+            B.adamw_mixed_bind([empty], [empty], [B.Adam8State.zeros(0)], hyper(), step_dev=step)]
+    for k, run in enumerate(runs):
+        run()
+        torch.cuda.synchronize()
+        assert step.tolist() == [k + 1, 0]
+    B.adamw_mixed_batched([empty], [empty], [(empty, empty)], hyper())
+    B.adam8_read_batched([B.Adam8State.zeros(0)], [empty], [empty])
+    B.adam8_write_batched([], [], [])
+    torch.cuda.synchronize()
+
+
+def test_same_inputs_same_bits():
+    """Two runs of several steps on many thread blocks give the same bits."""
+    import torch
+    from muon_optimizer_step_02_b200 import binding as B
+    runs = []
+    for _ in range(2):
+        c = Case([3 << 20, 4099, 77], FORMATS["mixed"], "bf16")
+        step = torch.zeros(2, dtype=torch.int32, device="cuda")
+        run = B.adamw_mixed_bind(c.P, c.G, c.S, hyper(beta2=0.999), c.E, c.C, DECAY,
+                                 step_dev=step, rounding="stochastic", seed=-1)
+        for _ in range(4):
+            run()
+        torch.cuda.synchronize()
+        runs.append(c.arrays() + [step])
+    for x, y in zip(*runs):
+        assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_a_coefficient_that_is_not_finite_skips_the_step(bad):
     import torch
