@@ -169,7 +169,7 @@ muon_status_t adam8_launch(const adam8_tensor_t* x, int n, int32_t dtype, bool w
   if (units == 0) return MUON_OK;
   a.n_seg = static_cast<uint32_t>(n);
   a.ubeg[n] = units;
-  const unsigned grid = grid_for(units, sms, 16);
+  const unsigned grid = grid_for(units, sms, write ? kA8WriteResident : kA8ReadResident);
   return write ? launch(adam8_write_kernel<kSegs>, a, grid, kMixThreads, st)
                : launch(adam8_read_kernel<kSegs>, a, grid, kMixThreads, st);
 }
