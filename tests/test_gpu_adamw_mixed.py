@@ -445,6 +445,28 @@ def test_past_32_bits_of_elements():
     del words
 
 
+def test_roots_are_correctly_rounded(tmp_path):
+    """Every fp32 value from 2^-98 up to the largest: the kernels' square root
+    equals the correctly rounded one."""
+    import ctypes
+    import os
+    import shutil
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    if not os.path.exists(nvcc):
+        pytest.skip("nvcc is not available")
+    lib = str(tmp_path / "root_check.so")
+    subprocess.run([nvcc, "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-std=c++17",
+                    "-Xcompiler", "-fPIC", "-shared", "--expt-relaxed-constexpr",
+                    "-I", os.path.join(root, "muon_optimizer_step_02_b200", "csrc"),
+                    "-o", lib, os.path.join(root, "tests", "cpp", "root_check.cu")], check=True)
+    check = ctypes.CDLL(lib).root_differences
+    check.argtypes, check.restype = [ctypes.c_uint32, ctypes.c_uint32], ctypes.c_longlong
+    first, end = (127 - 98) << 23, 255 << 23        # 2^-98, infinity
+    assert check(first, end - first) == 0
+
+
 # ---- the norm -----------------------------------------------------------------
 
 def norm_of(grads, limit=1.0, ws=None):
