@@ -258,7 +258,10 @@ __device__ __forceinline__ bool mixed_moments(const P& a, const MixStep& w, floa
 // what the weights need (parameters, averages) likewise, later.  fp32 arrays
 // are copied in 16-byte pieces, lane l taking pieces l and 32 + l (so that a
 // warp's access is one stretch of memory) where it reads 2 l and 2 l + 1; the
-// other arrays by the lane that will read them.  Places in a thread block's buffer:
+// other arrays by the lane that will read them.  Whatever the gradients' types
+// from one block to the next, a warp's part of every array is its own (256
+// fp32 values, or as many bf16 in its first half).  Places in a thread block's
+// buffer:
 constexpr int kBufG = 0, kBufCodes = 4096, kBufP = 6144, kBufE = 10240, kMixBuf = 14336;
 
 template <int kBytes>
@@ -286,11 +289,11 @@ __device__ __forceinline__ void from_buf_f32(uint32_t at, float2 (&x)[4]) {
                : "r"(at + threadIdx.x * 32 + 16) : "memory");
 }
 
-__device__ __forceinline__ void from_buf_bf16(uint32_t at, float2 (&x)[4]) {
+__device__ __forceinline__ void from_buf_bf16(uint32_t at, int lane, float2 (&x)[4]) {
   uint4 w;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-               : "r"(at + threadIdx.x * 16) : "memory");
+               : "r"(at + (threadIdx.x & ~31) * 32 + lane * 16) : "memory");
   unpack8(w, x);
 }
 
@@ -337,7 +340,7 @@ __device__ __forceinline__ void find_place(const P& a, uint32_t u, int warp, Mix
 __device__ __forceinline__ uint32_t fetch_moments(const MixSeg& s, const MixPlace& at,
                                                   uint32_t buf, int lane) {
   if (s.numel & kSegBf16)
-    copy_async<16>(buf + kBufG + threadIdx.x * 16,
+    copy_async<16>(buf + kBufG + (threadIdx.x & ~31) * 32 + lane * 16,
                    static_cast<const uint16_t*>(s.g) + at.i0 + lane * 8);
   else
     copy_f32(buf + kBufG, static_cast<const float*>(s.g) + at.i0, lane);
@@ -399,7 +402,7 @@ __device__ __forceinline__ void fetch_ragged(const MixSeg& s, const MixPlace& at
   for (int k = 0; k < 8; ++k) {
     const int j = k * 32 + lane, wide = first * 32 + j * 4;
     if (g16)
-      *reinterpret_cast<uint16_t*>(buf + kBufG + first * 16 + j * 2) =
+      *reinterpret_cast<uint16_t*>(buf + kBufG + first * 32 + j * 2) =
           static_cast<uint16_t>(__float_as_uint(g[k]) >> 16);
     else
       *reinterpret_cast<float*>(buf + kBufG + wide) = g[k];
@@ -424,7 +427,7 @@ __device__ __forceinline__ void mixed_block8(const P& a, const MixSeg& s, const 
   {
     float2 g[4], r[4];
     copies_wait<1>();
-    if (kG16) from_buf_bf16(buf + kBufG, g);
+    if (kG16) from_buf_bf16(buf + kBufG, lane, g);
     else from_buf_f32(buf + kBufG, g);
     const float mf = a8_factor(scale & 0xffu), rf = a8_factor(scale >> 8);
     const uint2 mw = from_buf_codes(buf + kBufCodes);
@@ -433,7 +436,7 @@ __device__ __forceinline__ void mixed_block8(const P& a, const MixSeg& s, const 
     a8_decode_m4(mw.y, mf, m + 2);
     a8_decode_r4(rw.x, rf, r);
     a8_decode_r4(rw.y, rf, r + 2);
-    if (!kG16) __syncwarp();   // before other lanes' pieces are replaced
+    __syncwarp();   // before other lanes' pieces are replaced
     next_moments();
     odd = mixed_moments<true>(a, w, g, m, r, nr);
   }
@@ -567,9 +570,9 @@ __device__ __forceinline__ void mixed_ragged32(const P& a, const MixSeg& s, cons
 // A thread block takes a unit of 4 blocks of 256 elements at a time, one warp
 // per block, so that everything about the tensor (table look-up, pointers) is
 // uniform over the thread block.  Full blocks of aligned tensors move 8
-// elements per lane at a time; ragged ends and unaligned
-// tensors go element by element.  Tensors with 8-bit states come first, in a
-// loop of their own (one loop for both forms spilled registers).
+// elements per lane at a time; ragged ends and unaligned tensors go element by
+// element.  Tensors with 8-bit states come first, in a loop of their own (one
+// loop for both forms spilled registers).
 template <bool kStochastic, int kSegs>
 __global__ void __launch_bounds__(kMixThreads, kMixResident)
 adamw_mixed_kernel(const __grid_constant__ MixParams<kSegs> a) {

@@ -68,7 +68,8 @@ class Case:
             m, v = (m * 0, v * 0) if empty else (m, v)
             self.P.append(self.new(p))
             g = torch.from_numpy(wl.adamw_grad(n, i, 1, seed, wid=300))
-            self.G.append(self.new.tensor(g.bfloat16() if grad == "bf16" else g))
+            half = grad == "bf16" or (grad == "both" and i % 3 != 1)
+            self.G.append(self.new.tensor(g.bfloat16() if half else g))
             if self.eight[i]:
                 (m8, mb), (r8, rb) = (ao.codes_f32(m, ao.M_BITS),
                                       ao.codes_f32(np.sqrt(v), ao.R_BITS))
@@ -262,6 +263,25 @@ def test_many_tensors_take_several_launches():
     torch.cuda.synchronize()
     assert step.tolist() == [4, 0]
     check(c, before, h, 4, rounding="stochastic", seed=9)
+
+
+@pytest.mark.parametrize("ema", [False, True])
+@pytest.mark.parametrize("form", ["8", "mixed"])
+def test_gradient_types_change_between_tensors(form, ema):
+    """A thread block goes from tensors with bf16 gradients to ones with fp32
+    gradients and back, full and ragged blocks in turn, while it copies one
+    block ahead: enough tensors of a few units that each block sees several."""
+    import torch
+    from muon_optimizer_step_02_b200 import binding as B
+    h = hyper()
+    sizes = [1024 * (20 + 7 * (i % 5)) + (0, 0, 300, 77)[i % 4] for i in range(380)]
+    c = Case(sizes, FORMATS[form], "both", ema=ema, copy=False)
+    run = B.adamw_mixed_bind(c.P, c.G, c.S, h, c.E, c.C, DECAY, rounding="stochastic", seed=8)
+    for t in (1, 2):
+        before = c.snapshot()
+        run(step_now=t)
+        torch.cuda.synchronize()
+        check(c, before, h, t, rounding="stochastic", seed=8)
 
 
 def test_a_call_without_elements_counts_its_step():
