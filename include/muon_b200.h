@@ -303,7 +303,7 @@ typedef struct {
  *        step_dev points to two device int32: the steps taken so far (t is
  *        one more; the call advances it) and a word for the call's own use,
  *        zero before the first call.  One captured CUDA graph then serves
- *        every step.  Calls that share a counter must be ordered.
+ *        every step.  Two calls of one step need a counter each.
  *  lr_dev    NULL, or a device float read in place of hyper->lr.
  *  coef_dev  NULL (c = 1), or a device float c, such as the second result of
  *        grad_norm_batched.  If it is not finite the call changes nothing,

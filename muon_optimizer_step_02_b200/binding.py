@@ -653,7 +653,8 @@ def adamw_mixed_bind(params: Sequence, grads: Sequence, states: Sequence, hyper,
     grad_scale: one fp32 that multiplies the gradients, such as out[1:] of
     grad_norm_bind; a value that is not finite skips the step.  rounding
     ("nearest" or "stochastic") and seed: how new moments go to 8 bits; calls
-    on different tensors want different seeds."""
+    on different tensors want different seeds, and counters of their own.  The
+    callable keeps the tensors alive; they must stay in place."""
     import torch
     f32 = (torch.float32,)
     n = len(params)

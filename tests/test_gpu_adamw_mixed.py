@@ -55,15 +55,18 @@ def host(t):
 
 class Case:
     """Tensors of one call with their host copies.  eight(i): whether tensor i
-    has an 8-bit state."""
+    has an 8-bit state; shift: elements that its arrays lie off their buffers'
+    starts, or a function of i."""
 
     def __init__(self, sizes, eight, grad="f32", ema=True, copy=True, shift=0, seed=0, empty=False):
         import torch
         from muon_optimizer_step_02_b200 import binding as B
-        self.sizes, self.new = sizes, Arrays(shift)
+        self.sizes, self.new = sizes, Arrays()
+        shift = shift if callable(shift) else lambda i, k=shift: k
         self.eight = [bool(eight(i)) for i in range(len(sizes))]
         self.P, self.G, self.S, self.E, self.C = [], [], [], [], []
         for i, n in enumerate(sizes):
+            self.new.shift = shift(i)
             p, m, v, e = wl.adamw_state(n, i, seed, wid=300)
             m, v = (m * 0, v * 0) if empty else (m, v)
             self.P.append(self.new(p))
@@ -276,6 +279,23 @@ def test_gradient_types_change_between_tensors(form, ema):
     h = hyper()
     sizes = [1024 * (20 + 7 * (i % 5)) + (0, 0, 300, 77)[i % 4] for i in range(380)]
     c = Case(sizes, FORMATS[form], "both", ema=ema, copy=False)
+    run = B.adamw_mixed_bind(c.P, c.G, c.S, h, c.E, c.C, DECAY, rounding="stochastic", seed=8)
+    for t in (1, 2):
+        before = c.snapshot()
+        run(step_now=t)
+        torch.cuda.synchronize()
+        check(c, before, h, t, rounding="stochastic", seed=8)
+
+
+@pytest.mark.parametrize("form", list(FORMATS))
+def test_alignment_changes_between_tensors(form):
+    """Aligned and unaligned tensors (off by 1 to 16 elements, so that some arrays
+    are and others are not aligned), ragged or not, in turn."""
+    import torch
+    from muon_optimizer_step_02_b200 import binding as B
+    h = hyper()
+    sizes = [1024 * (9 + 5 * (i % 4)) + (0, 256, 300, 77, 0)[i % 5] for i in range(390)]
+    c = Case(sizes, FORMATS[form], "both", shift=lambda i: (0, 0, 1, 0, 4, 8, 0, 16)[i % 8])
     run = B.adamw_mixed_bind(c.P, c.G, c.S, h, c.E, c.C, DECAY, rounding="stochastic", seed=8)
     for t in (1, 2):
         before = c.snapshot()
@@ -598,17 +618,19 @@ def test_reading_every_code_under_every_byte(dtype, shift):
     new.check_guards()
 
 
-@pytest.mark.parametrize("shift", [0, 1])
-@pytest.mark.parametrize("sizes", [SIZES, [(5 * i) % 41 for i in range(1100)]])
+@pytest.mark.parametrize("shift", [0, 1, None])
+@pytest.mark.parametrize("sizes", [SIZES, [(5 * i) % 41 for i in range(1100)],
+                                   [1024 * (9 + i % 7) + 100 * (i % 3) for i in range(450)]])
 def test_writing_and_reading_back(sizes, shift):
     """fp32 moments to the nearest codes, bit for bit; read back in bf16 and
     written again they give the same values; a state read in fp32 squares its
     roots."""
     import torch
     from muon_optimizer_step_02_b200 import binding as B
-    new = Arrays(shift)
+    new = Arrays()
     states, M, V, M16, R16 = [], [], [], [], []
     for i, n in enumerate(sizes):
+        new.shift = (0, 1, 0, 4, 8)[i % 5] if shift is None else shift
         _, m, v, _ = wl.adamw_state(n, i, 3, wid=301)
         M.append(new(m))
         V.append(new(v))
@@ -751,6 +773,48 @@ def test_calls_see_what_ran_before_them(n):
         results.append(arrays + after)
     for x, y, z in zip(*results):
         assert torch.equal(x, y) and torch.equal(x, z)
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """A process whose first calls are captured ones: no warm-up is needed."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import types, torch
+from muon_optimizer_step_02_b200 import binding as B
+h = types.SimpleNamespace(lr=0.01, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1)
+def side():
+    g = torch.Generator(device="cuda").manual_seed(1)
+    P = [torch.randn(n, generator=g, device="cuda") for n in (5000, 300)]
+    G = [torch.randn(n, generator=g, device="cuda") for n in (5000, 300)]
+    S = [B.Adam8State.zeros(5000), (torch.zeros(300, device="cuda"), torch.zeros(300, device="cuda"))]
+    out, step = torch.zeros(2, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    V = [torch.ones(5000, device="cuda") for _ in range(2)]
+    calls = [B.adam8_write_bind(S[:1], V[:1], V[1:]), B.grad_norm_bind(G, 1.0, out, B.grad_norm_workspace()),
+             B.adamw_mixed_bind(P, G, S, h, step_dev=step, grad_scale=out[1:], rounding="stochastic"),
+             B.adam8_read_bind(S[:1], V[:1], V[1:])]
+    return calls, [*P, S[0].exp_avg, S[0].root, S[0].scale, *S[1], out, step, *V]
+calls, a = side()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    for c in calls:
+        c()
+graph.replay()
+torch.cuda.synchronize()
+calls, b = side()
+for c in calls:
+    c()
+torch.cuda.synchronize()
+assert b[-3].tolist() == [1, 0], b[-3]
+assert all(torch.equal(x, y) for x, y in zip(a, b))
+print("captured first")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                         timeout=300)
+    assert res.returncode == 0 and "captured first" in res.stdout, res.stderr[-2000:]
 
 
 def test_interleaved_with_the_other_optimizer_calls():
