@@ -324,8 +324,7 @@ muon_status_t adamw_mixed_batched(const adamw_mixed_tensor_t *tensors, int32_t n
                                   const float *coef_dev, muon_stream_t stream);
 
 /* One gradient of grad_norm_batched: a device array of numel elements, fp32
- * (4-byte aligned) or bf16 (2-byte aligned); 16-byte aligned arrays take the
- * vectorised path. */
+ * (4-byte aligned) or bf16 (2-byte aligned). */
 typedef struct {
   const void *grad;
   int64_t numel;

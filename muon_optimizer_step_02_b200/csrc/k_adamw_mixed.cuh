@@ -289,6 +289,27 @@ __device__ __forceinline__ void from_buf_f32(uint32_t at, float2 (&x)[4]) {
                : "r"(at + threadIdx.x * 32 + 16) : "memory");
 }
 
+__device__ __forceinline__ void to_buf_f32(uint32_t at, const float2 (&x)[4]) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + threadIdx.x * 32),
+               "f"(x[0].x), "f"(x[0].y), "f"(x[1].x), "f"(x[1].y)
+               : "memory");
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + threadIdx.x * 32 + 16),
+               "f"(x[2].x), "f"(x[2].y), "f"(x[3].x), "f"(x[3].y)
+               : "memory");
+}
+
+__device__ __forceinline__ float word_of_buf(uint32_t at) {
+  float x;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+  return x;
+}
+
+__device__ __forceinline__ uint8_t byte_of_buf(uint32_t at) {
+  uint32_t x;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return static_cast<uint8_t>(x);
+}
+
 __device__ __forceinline__ void from_buf_bf16(uint32_t at, int lane, float2 (&x)[4]) {
   uint4 w;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -448,19 +469,26 @@ __device__ __forceinline__ void mixed_block8(const P& a, const MixSeg& s, const 
     mixed_weights(a, w, m, nr, p);
     if (s.e) mixed_average(a, p, e);
     __syncwarp();   // before other lanes' pieces are replaced
-    next_weights();
     if (at.full) {
+      next_weights();
       store8(s.p + i, p);
       if (s.c) store8_bf16(s.c + i, p);
       if (s.e) store8(s.e + i, e);
     } else {
+      // through shared memory, so that a warp's stores are one stretch (from
+      // the lanes' 8 elements each, 16.8 M unaligned elements took 200 us)
+      to_buf_f32(buf + kBufP, p);
+      if (s.e) to_buf_f32(buf + kBufE, e);
+      __syncwarp();
+      const uint32_t own = buf + (threadIdx.x & ~31) * 32 + lane * 4;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int j = lane * 8 + k;
+        const int j = k * 32 + lane;
         if (j >= at.left) continue;
-        s.p[at.i0 + j] = ::muonb200::at(p, k);
-        if (s.c) s.c[at.i0 + j] = __bfloat16_as_ushort(__float2bfloat16_rn(::muonb200::at(p, k)));
-        if (s.e) s.e[at.i0 + j] = ::muonb200::at(e, k);
+        const float y = word_of_buf(own + kBufP + k * 128);
+        s.p[at.i0 + j] = y;
+        if (s.c) s.c[at.i0 + j] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+        if (s.e) s.e[at.i0 + j] = word_of_buf(own + kBufE + k * 128);
       }
     }
   }
@@ -493,13 +521,23 @@ __device__ __forceinline__ void mixed_block8(const P& a, const MixSeg& s, const 
     store8_codes(cm + i, m8);
     store8_codes(cr + i, r8);
   } else {
+    __syncwarp();
+    const uint32_t own = buf + kBufP + (threadIdx.x & ~31) * 32;
+    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(own + lane * 8), "r"(m8[0]), "r"(m8[1])
+                 : "memory");
+    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(own + 256 + lane * 8), "r"(r8[0]),
+                 "r"(r8[1])
+                 : "memory");
+    __syncwarp();
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int j = lane * 8 + k;
+      const int j = k * 32 + lane;
       if (j >= at.left) continue;
-      cm[at.i0 + j] = static_cast<uint8_t>(m8[k >> 2] >> (8 * (k & 3)));
-      cr[at.i0 + j] = static_cast<uint8_t>(r8[k >> 2] >> (8 * (k & 3)));
+      cm[at.i0 + j] = byte_of_buf(own + j);
+      cr[at.i0 + j] = byte_of_buf(own + 256 + j);
     }
+    __syncwarp();
+    next_weights();
   }
   if (lane == 0) {
     if (at.full) {

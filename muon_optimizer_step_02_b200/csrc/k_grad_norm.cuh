@@ -38,9 +38,11 @@ constexpr int kNormResident = 8;      // thread blocks per SM (32 registers)
 constexpr int kNormMaxSegs = 1300;    // 1300 x 20 bytes of kernel parameters
 constexpr int kNormMaxGrid = 2048;
 
+// A tensor from its first 16-byte boundary on, and the up to 7 elements before
+// it, which are taken apart (squares may be added in any order).
 struct NormSeg {
   const void* g;
-  unsigned long long numel;   // and the flags kSegBf16, kSegVec
+  unsigned long long numel;   // from g on; their number before g (kSegPlace), kSegBf16
 };
 
 struct NormWorkspace {
@@ -81,7 +83,7 @@ __device__ __forceinline__ void add_squares(const float2 (&g)[4], double (&sum)[
   }
 }
 
-// kCount whole chunks of an aligned gradient from element i0 on, requested
+// kCount whole chunks of a gradient from element i0 on, requested
 // before the first is used.
 template <int kCount, bool kG16>
 __device__ __forceinline__ void add_chunks(const void* g, long long i0, double (&sum)[4]) {
@@ -133,15 +135,14 @@ grad_norm_kernel(const __grid_constant__ NormParams<kSegs> a) {
     long long i0 = static_cast<long long>(u - a.ubeg[cur]) * kNormUnit;
     long long left = static_cast<long long>(s.numel & kSegNumel) - i0;
     const bool g16 = (s.numel & kSegBf16) != 0;
-    const bool vec = (s.numel & kSegVec) != 0;
-    if (vec && left >= kNormUnit) {
+    if (left >= kNormUnit) {
       if (g16) add_chunks<kNormDeep, true>(s.g, i0, sum);
       else add_chunks<kNormDeep, false>(s.g, i0, sum);
       continue;
     }
-    // a tensor's last unit, or one that is not aligned: chunk by chunk
+    // a tensor's last unit: chunk by chunk
     for (int c = 0; c < kNormDeep && left > 0; ++c, i0 += kNormChunk, left -= kNormChunk) {
-      if (vec && left >= kNormChunk) {
+      if (left >= kNormChunk) {
         if (g16) add_chunks<1, true>(s.g, i0, sum);
         else add_chunks<1, false>(s.g, i0, sum);
         continue;
@@ -157,7 +158,18 @@ grad_norm_kernel(const __grid_constant__ NormParams<kSegs> a) {
       add_squares(g, sum);
     }
   }
-  double total = block_sum((sum[0] + sum[1]) + (sum[2] + sum[3]), sh[0]);
+  double total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  for (uint32_t c = blockIdx.x; c < a.n_seg; c += gridDim.x) {
+    const NormSeg& s = a.seg[c];
+    const uint32_t before = static_cast<uint32_t>(s.numel >> kSegPlace) & 7u;
+    if (threadIdx.x < before) {
+      const long long i = static_cast<long long>(threadIdx.x) - before;
+      const double x = static_cast<double>(
+          s.numel & kSegBf16 ? bf16_at(s.g, i) : static_cast<const float*>(s.g)[i]);
+      total = fma(x, x, total);
+    }
+  }
+  total = block_sum(total, sh[0]);
   if (threadIdx.x == 0) {
     a.ws->part[blockIdx.x] = total;
     __threadfence();

@@ -141,9 +141,16 @@ muon_status_t norm_launch(const grad_tensor_t* x, int n, double max_norm, NormWo
   uint32_t units = 0;
   for (int i = 0; i < n; ++i) {
     const bool g16 = x[i].dtype == MUON_BF16;
-    a.seg[i] = NormSeg{x[i].grad, flagged(x[i].numel, g16, (bits(x[i].grad) & 15u) == 0)};
+    const int size = g16 ? 2 : 4;
+    const int64_t before = std::min<int64_t>(
+        x[i].numel, static_cast<int64_t>((-bits(x[i].grad) & 15u) / size));
+    const int64_t from = x[i].numel - before;
+    a.seg[i] = NormSeg{static_cast<const char*>(x[i].grad) + before * size,
+                       flagged(from, g16, false) |
+                           static_cast<unsigned long long>(before) << kSegPlace};
     a.ubeg[i] = units;
-    units += units_of(x[i].numel, kNormUnit);
+    // (one unit at least, so that many small tensors spread over the grid)
+    units += x[i].numel > 0 ? std::max(1u, units_of(from, kNormUnit)) : 0u;
   }
   a.n_seg = static_cast<uint32_t>(n);
   a.ubeg[n] = units;
