@@ -344,6 +344,11 @@ struct MixPlace {
   bool full;           // a full block of an aligned tensor
 };
 
+// Elements of the tensor in a place's block.
+__device__ __forceinline__ int block_elements(const MixPlace& at) {
+  return at.left < kA8Block ? static_cast<int>(at.left) : kA8Block;
+}
+
 template <class P>
 __device__ __forceinline__ void find_place(const P& a, uint32_t u, int warp, MixPlace& at) {
   if (u >= at.end) {
@@ -404,33 +409,41 @@ __device__ __forceinline__ void mixed_average(const P& a, const float2 (&p)[4], 
 __device__ __forceinline__ void fetch_ragged(const MixSeg& s, const MixPlace& at,
                                              unsigned char* buf, int lane) {
   const bool g16 = (s.numel & kSegBf16) != 0;
-  float p[8], g[8], e[8];
-  uint32_t m[8], r[8];
+  const int n = block_elements(at);
+  const long long i = at.i0 + lane;
+  const float* sp = s.p + i;
+  const float* se = s.e ? s.e + i : sp;      // (read, and not used, without an average)
+  const uint8_t* sm = static_cast<uint8_t*>(s.m) + i;
+  const uint8_t* sr = static_cast<uint8_t*>(s.v) + i;
+  const uint16_t* g2 = static_cast<const uint16_t*>(s.g) + i;
+  const float* g4 = static_cast<const float*>(s.g) + i;
+  float p[8], e[8];
+  uint32_t g[8], m[8], r[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {   // everything is requested before the first use
-    const int j = k * 32 + lane;
-    const bool in = j < at.left;
-    const long long i = at.i0 + j;
-    g[k] = !in ? 0.f : g16 ? bf16_at(s.g, i) : static_cast<const float*>(s.g)[i];
-    m[k] = in ? static_cast<uint8_t*>(s.m)[i] : 0u;
-    r[k] = in ? static_cast<uint8_t*>(s.v)[i] : 0u;
-    p[k] = in ? s.p[i] : 0.f;
-    e[k] = in && s.e ? s.e[i] : 0.f;
+    const bool in = k * 32 + lane < n;
+    g[k] = 0u;
+    if (in) g[k] = g16 ? g2[k * 32] : __float_as_uint(g4[k * 32]);
+    m[k] = in ? sm[k * 32] : 0u;
+    r[k] = in ? sr[k * 32] : 0u;
+    p[k] = in ? sp[k * 32] : 0.f;
+    e[k] = in ? se[k * 32] : 0.f;
   }
   __syncwarp();   // the lanes have read the block before
   const int first = threadIdx.x & ~31;
+  unsigned char* wide = buf + first * 32 + lane * 4;
+  unsigned char* codes = buf + kBufCodes + first * 8 + lane;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const int j = k * 32 + lane, wide = first * 32 + j * 4;
     if (g16)
-      *reinterpret_cast<uint16_t*>(buf + kBufG + first * 32 + j * 2) =
-          static_cast<uint16_t>(__float_as_uint(g[k]) >> 16);
+      *reinterpret_cast<uint16_t*>(buf + kBufG + first * 32 + lane * 2 + k * 64) =
+          static_cast<uint16_t>(g[k]);
     else
-      *reinterpret_cast<float*>(buf + kBufG + wide) = g[k];
-    buf[kBufCodes + first * 8 + j] = static_cast<uint8_t>(m[k]);
-    buf[kBufCodes + kMixThreads * 8 + first * 8 + j] = static_cast<uint8_t>(r[k]);
-    *reinterpret_cast<float*>(buf + kBufP + wide) = p[k];
-    *reinterpret_cast<float*>(buf + kBufE + wide) = e[k];
+      *reinterpret_cast<uint32_t*>(wide + kBufG + k * 128) = g[k];
+    codes[k * 32] = static_cast<uint8_t>(m[k]);
+    codes[kMixThreads * 8 + k * 32] = static_cast<uint8_t>(r[k]);
+    *reinterpret_cast<float*>(wide + kBufP + k * 128) = p[k];
+    *reinterpret_cast<float*>(wide + kBufE + k * 128) = e[k];
   }
   __syncwarp();
 }
@@ -476,27 +489,32 @@ __device__ __forceinline__ void mixed_block8(const P& a, const MixSeg& s, const 
       if (s.e) store8(s.e + i, e);
     } else {
       // through shared memory, so that a warp's stores are one stretch (from
-      // the lanes' 8 elements each, 16.8 M unaligned elements took 200 us)
+      // the lanes' 8 elements each, 16.8 M unaligned elements took 200 us, now
+      // 104; aligned ones 45-50)
       to_buf_f32(buf + kBufP, p);
       if (s.e) to_buf_f32(buf + kBufE, e);
       __syncwarp();
       const uint32_t own = buf + (threadIdx.x & ~31) * 32 + lane * 4;
+      const int n = block_elements(at);
+      float* sp = s.p + at.i0 + lane;
+      uint16_t* sc = s.c + at.i0 + lane;
+      float* se = s.e + at.i0 + lane;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int j = k * 32 + lane;
-        if (j >= at.left) continue;
+        if (k * 32 + lane >= n) continue;
         const float y = word_of_buf(own + kBufP + k * 128);
-        s.p[at.i0 + j] = y;
-        if (s.c) s.c[at.i0 + j] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
-        if (s.e) s.e[at.i0 + j] = word_of_buf(own + kBufE + k * 128);
+        sp[k * 32] = y;
+        if (s.c) sc[k * 32] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+        if (s.e) se[k * 32] = word_of_buf(own + kBufE + k * 128);
       }
     }
   }
   if (!at.full) {
     // past the tensor's end nothing enters the block's largest
+    const int n = block_elements(at) - lane * 8;
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (lane * 8 + k >= at.left) ::muonb200::at(m, k) = ::muonb200::at(nr, k) = 0.f;
+      if (k >= n) ::muonb200::at(m, k) = ::muonb200::at(nr, k) = 0.f;
     odd = true;
   }
   uint32_t x[8], m8[2], r8[2], mbyte, rbyte;
@@ -529,12 +547,14 @@ __device__ __forceinline__ void mixed_block8(const P& a, const MixSeg& s, const 
                  "r"(r8[1])
                  : "memory");
     __syncwarp();
+    const int n = block_elements(at);
+    cm += at.i0 + lane;
+    cr += at.i0 + lane;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int j = k * 32 + lane;
-      if (j >= at.left) continue;
-      cm[at.i0 + j] = byte_of_buf(own + j);
-      cr[at.i0 + j] = byte_of_buf(own + 256 + j);
+      if (k * 32 + lane >= n) continue;
+      cm[k * 32] = byte_of_buf(own + lane + k * 32);
+      cr[k * 32] = byte_of_buf(own + 256 + lane + k * 32);
     }
     __syncwarp();
     next_weights();
