@@ -784,6 +784,7 @@ adam8_write_kernel(const __grid_constant__ A8Params<kSegs> a) {
     const long long i0 = static_cast<long long>(blk) * kA8Block;
     const long long left = static_cast<long long>(s.numel & kSegNumel) - i0;
     if (left <= 0) continue;
+    const int n = left < kA8Block ? static_cast<int>(left) : kA8Block;
     const bool vec = (s.numel & kSegVec) && left >= kA8Block;
     const bool b16 = (s.numel & kSegBf16) != 0;
     const long long iv = i0 + lane * 8;
@@ -797,12 +798,15 @@ adam8_write_kernel(const __grid_constant__ A8Params<kSegs> a) {
         load8(static_cast<float*>(s.v) + iv, r);
       }
     } else {
+      const uint16_t *m2 = static_cast<uint16_t*>(s.m) + i0 + lane,
+                     *v2 = static_cast<uint16_t*>(s.v) + i0 + lane;
+      const float *m4 = static_cast<float*>(s.m) + i0 + lane,
+                  *v4 = static_cast<float*>(s.v) + i0 + lane;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int j = k * 32 + lane;
-        const bool in = j < left;
-        at(m, k) = !in ? 0.f : b16 ? bf16_at(s.m, i0 + j) : static_cast<float*>(s.m)[i0 + j];
-        at(r, k) = !in ? 0.f : b16 ? bf16_at(s.v, i0 + j) : static_cast<float*>(s.v)[i0 + j];
+        const bool in = k * 32 + lane < n;
+        at(m, k) = !in ? 0.f : b16 ? bf16_at(m2, k * 32) : m4[k * 32];
+        at(r, k) = !in ? 0.f : b16 ? bf16_at(v2, k * 32) : v4[k * 32];
       }
     }
     // r: the roots with a minus sign
@@ -825,12 +829,12 @@ adam8_write_kernel(const __grid_constant__ A8Params<kSegs> a) {
       store8_codes(s.m8 + iv, m8);
       store8_codes(s.r8 + iv, r8);
     } else {
+      uint8_t *cm = s.m8 + i0 + lane, *cr = s.r8 + i0 + lane;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int j = k * 32 + lane;
-        if (j >= left) continue;
-        s.m8[i0 + j] = static_cast<uint8_t>(m8[k >> 2] >> (8 * (k & 3)));
-        s.r8[i0 + j] = static_cast<uint8_t>(r8[k >> 2] >> (8 * (k & 3)));
+        if (k * 32 + lane >= n) continue;
+        cm[k * 32] = static_cast<uint8_t>(m8[k >> 2] >> (8 * (k & 3)));
+        cr[k * 32] = static_cast<uint8_t>(r8[k >> 2] >> (8 * (k & 3)));
       }
     }
     if (lane == 0) {
@@ -898,20 +902,29 @@ adam8_read_kernel(const __grid_constant__ A8Params<kSegs> a) {
       }
     } else if (at.left > 0) {
       const float mf = a8_factor(s.s[2ll * at.blk]), rf = a8_factor(s.s[2ll * at.blk + 1]);
+      const int n = block_elements(at);
+      const long long i = at.i0 + lane;
+      uint32_t cm[8], cr[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int j = k * 32 + lane;
-        if (j >= at.left) continue;
-        const long long i = at.i0 + j;
+        const bool in = k * 32 + lane < n;
+        cm[k] = in ? (s.m8 + i)[k * 32] : 0u;
+        cr[k] = in ? (s.r8 + i)[k * 32] : 0u;
+      }
+      uint16_t *m2 = static_cast<uint16_t*>(s.m) + i, *v2 = static_cast<uint16_t*>(s.v) + i;
+      float *m4 = static_cast<float*>(s.m) + i, *v4 = static_cast<float*>(s.v) + i;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (k * 32 + lane >= n) continue;
         float2 x[2], y[2];
-        a8_decode_m4(s.m8[i], mf, x);
-        a8_decode_r4(s.r8[i], rf, y);
+        a8_decode_m4(cm[k], mf, x);
+        a8_decode_r4(cr[k], rf, y);
         if (b16) {
-          static_cast<uint16_t*>(s.m)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x[0].x));
-          static_cast<uint16_t*>(s.v)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(y[0].x));
+          m2[k * 32] = __bfloat16_as_ushort(__float2bfloat16_rn(x[0].x));
+          v2[k * 32] = __bfloat16_as_ushort(__float2bfloat16_rn(y[0].x));
         } else {
-          static_cast<float*>(s.m)[i] = x[0].x;
-          static_cast<float*>(s.v)[i] = y[0].x * y[0].x;
+          m4[k * 32] = x[0].x;
+          v4[k * 32] = y[0].x * y[0].x;
         }
       }
     }
