@@ -2,6 +2,7 @@
 conversions of its states, through the binding, against the 64-bit oracle and,
 where the library fixes every rounding (moments and codes), bit for bit
 against its restatement in 32 bits."""
+import os
 import types
 
 import numpy as np
@@ -304,6 +305,45 @@ def test_alignment_changes_between_tensors(form):
         check(c, before, h, t, rounding="stochastic", seed=8)
 
 
+@pytest.mark.parametrize("case", range(int(os.environ.get("MUONB200_FUZZ_MIXED_CASES", "10"))))
+def test_random_calls(case):
+    """Random lists of tensors (sizes, state forms, gradient types, alignments),
+    settings, coefficients, factors and steps, against the oracles."""
+    import torch
+    from muon_optimizer_step_02_b200 import binding as B
+    r = np.random.default_rng(1000 + case)
+    count = int(np.exp(r.uniform(0, np.log(500))))
+    top = np.log(3e5 if count > 30 else 3e6)
+    sizes = [int(np.exp(r.uniform(0, top))) for _ in range(count)]
+    while sum(sizes) > 6_000_000:
+        sizes.pop(int(np.argmax(sizes)))
+    sizes = sizes or [1]
+    n = len(sizes)
+    eight, off = r.random(n) < r.choice([0.0, 0.5, 1.0]), r.choice([0, 0, 0, 1, 2, 4, 8], n)
+    c = Case(sizes, lambda i: eight[i], r.choice(["f32", "bf16", "both"]), ema=bool(r.random() < 0.6),
+             copy=bool(r.random() < 0.6), shift=lambda i: int(off[i]), seed=case,
+             empty=bool(r.random() < 0.3))
+    h = hyper(lr=float(10 ** r.uniform(-4, -1)), beta1=float(r.choice([0.0, 0.9, 0.95])),
+              beta2=float(r.choice([0.9, 0.95, 0.99, 0.999])), eps=float(r.choice([1e-8, 1e-12])),
+              weight_decay=float(r.choice([0.0, 0.1])))
+    rounding, seed = str(r.choice(["nearest", "stochastic"])), int(r.integers(0, 1 << 62))
+    ls, ws = ([float(x) for x in r.choice([0.25, 0.5, 1.0, 2.0], n)] for _ in range(2))
+    coef = float(np.float32(r.choice([1.0, r.uniform(0.01, 1.0)])))
+    step = torch.tensor([int(r.choice([0, 5, 12345])), 0], dtype=torch.int32, device="cuda")
+    run = B.adamw_mixed_bind(c.P, c.G, c.S, h, c.E, c.C, DECAY, step_dev=step, lr_scales=ls,
+                             wd_scales=ws, rounding=rounding, seed=seed,
+                             grad_scale=torch.tensor([coef], device="cuda"))
+    for _ in range(2):
+        before, t = c.snapshot(), step[0].item() + 1
+        run()
+        torch.cuda.synchronize()
+        assert step.tolist() == [t, 0]
+        check(c, before, h, t, coef, ls, ws, rounding, seed)
+    norm, k = ao.grad_norm([host(g) for g in c.G], 0.1)
+    got = norm_of(c.G, 0.1)
+    assert near(got[0], norm) and near(got[1], k)
+
+
 def test_a_call_without_elements_counts_its_step():
     import torch
     from muon_optimizer_step_02_b200 import binding as B
@@ -489,7 +529,6 @@ def test_roots_are_correctly_rounded(tmp_path):
     """Every fp32 value from 2^-98 up to the largest: the kernels' square root
     equals the correctly rounded one."""
     import ctypes
-    import os
     import shutil
     import subprocess
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -777,7 +816,6 @@ def test_calls_see_what_ran_before_them(n):
 
 def test_first_calls_of_a_process_may_be_captured():
     """A process whose first calls are captured ones: no warm-up is needed."""
-    import os
     import subprocess
     import sys
     code = """
