@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 from ctypes import (POINTER, Structure, c_char_p, c_double, c_float, c_int32,
                     c_int64, c_size_t, c_uint64, c_void_p)
 from typing import List, Optional, Sequence, Tuple
@@ -638,7 +639,7 @@ def adamw_mixed_bind(params: Sequence, grads: Sequence, states: Sequence, hyper,
                      ema_decay: float = 0.0, step: int = 1, step_dev=None, lr_dev=None,
                      grad_scale=None, lr_scales: Optional[Sequence[float]] = None,
                      wd_scales: Optional[Sequence[float]] = None,
-                     rounding: str = "nearest", seed: int = 0):
+                     rounding: Optional[str] = None, seed: int = 0):
     """Marshals adamw_mixed_batched once and returns `run(step_now=None,
     stream=None)`.  All tensors contiguous, on one CUDA device, none sharing
     memory with another.
@@ -653,8 +654,12 @@ def adamw_mixed_bind(params: Sequence, grads: Sequence, states: Sequence, hyper,
     grad_scale: one fp32 that multiplies the gradients, such as out[1:] of
     grad_norm_bind; a value that is not finite skips the step.  rounding
     ("nearest" or "stochastic") and seed: how new moments go to 8 bits; calls
-    on different tensors want different seeds, and counters of their own.  The
-    callable keeps the tensors alive; they must stay in place."""
+    on different tensors want different seeds, and counters of their own.
+    Training wants "stochastic": over many steps nearest rounding leaves
+    first moments whose gradients stopped above zero, so that their parameters
+    go on moving, and roots far from AdamW's (muon_round_t in the header says
+    how far).  None is "nearest", with a warning if there is an Adam8State.
+    The callable keeps the tensors alive; they must stay in place."""
     import torch
     f32 = (torch.float32,)
     n = len(params)
@@ -667,6 +672,12 @@ def adamw_mixed_bind(params: Sequence, grads: Sequence, states: Sequence, hyper,
         raise ValueError("one grad, state, ema, copy and scale entry per param")
     if int(step) > 0x7FFFFFFF:
         raise ValueError(f"step {step} does not fit 32 bits")
+    if rounding is None:
+        rounding = "nearest"
+        if any(isinstance(s, Adam8State) for s in states):
+            warnings.warn("8-bit moments rounded to the nearest lose track of AdamW over many "
+                          "steps: pass rounding='stochastic' to train, or rounding='nearest' if "
+                          "it is meant", stacklevel=2)
     if rounding not in _ROUNDINGS:
         raise ValueError(f"rounding must be one of {sorted(_ROUNDINGS)}, got {rounding!r}")
     dev = next((t.device for t in (*params, step_dev) if isinstance(t, torch.Tensor)), None)
