@@ -254,7 +254,9 @@ typedef enum { MUON_F32 = 0, MUON_BF16 = 1 } muon_dtype_t;
 typedef enum { MUON_ROUND_NEAREST = 0, MUON_ROUND_STOCHASTIC = 1 } muon_round_t;
 
 /* Settings of adamw_mixed_batched.  lr, weight_decay, ema_decay finite;
- * beta1, beta2 in [0, 1); eps >= 0.  seed gives the random bits of
+ * beta1, beta2 in [0, 1); eps 0 or at least 2^-126 (fp32's least normal
+ * value).  With eps = 0 an element whose moments are zero becomes NaN, as the
+ * formula's 0 / 0.  seed gives the random bits of
  * stochastic rounding, with the step number, the tensor's place in the call
  * and the element's place in the tensor: the same call on the same inputs
  * gives the same bits, and calls on different tensors want different seeds. */

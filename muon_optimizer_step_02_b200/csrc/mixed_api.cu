@@ -20,6 +20,10 @@ namespace {
 constexpr int64_t kMaxElements = int64_t{1} << 39;   // of one call: blocks count in 32 bits
 constexpr int kFewSegs = 16;   // launches of few tensors carry a short table
 
+// The kernel's division takes a denominator below fp32's normal range for 0,
+// which an eps down there would leave of elements without moments.
+constexpr double kLeastEps = 0x1p-126;
+
 inline uintptr_t bits(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 
 inline uint32_t units_of(int64_t numel, int unit) {
@@ -225,8 +229,10 @@ muon_status_t adamw_mixed_batched(const adamw_mixed_tensor_t* tensors, int32_t n
   if (n_tensors < 0 || !hyper || (n_tensors > 0 && !tensors)) return MUON_ERR_INVALID_ARG;
   const adamw_mixed_hyper_t& h = *hyper;
   if (!std::isfinite(h.lr) || !std::isfinite(h.weight_decay) || !std::isfinite(h.eps) ||
-      h.eps < 0.0 || !std::isfinite(h.ema_decay) || !(h.beta1 >= 0.0 && h.beta1 < 1.0) ||
+      !std::isfinite(h.ema_decay) || !(h.beta1 >= 0.0 && h.beta1 < 1.0) ||
       !(h.beta2 >= 0.0 && h.beta2 < 1.0))
+    return MUON_ERR_INVALID_ARG;
+  if (h.eps != 0.0 && !(h.eps >= kLeastEps))
     return MUON_ERR_INVALID_ARG;
   if (h.rounding != MUON_ROUND_NEAREST && h.rounding != MUON_ROUND_STOCHASTIC)
     return MUON_ERR_INVALID_ARG;
