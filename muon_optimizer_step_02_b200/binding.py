@@ -518,6 +518,13 @@ def _dense(t, dtypes, numel, what, device=None, i=None):
     raise ValueError(f"{what} is on {t.device}, expected {device}")
 
 
+def _int32(x, what):
+    x = int(x)
+    if not -0x80000000 <= x <= 0x7FFFFFFF:
+        raise ValueError(f"{what} {x} does not fit 32 bits")
+    return x
+
+
 def _name(what, i):
     return what if i is None else what.format(i)
 
@@ -670,8 +677,7 @@ def adamw_mixed_bind(params: Sequence, grads: Sequence, states: Sequence, hyper,
     if not (len(grads) == len(states) == len(emas) == len(copies) == len(lr_scales)
             == len(wd_scales) == n):
         raise ValueError("one grad, state, ema, copy and scale entry per param")
-    if int(step) > 0x7FFFFFFF:
-        raise ValueError(f"step {step} does not fit 32 bits")
+    step = _int32(step, "step")
     if rounding is None:
         rounding = "nearest"
         if any(isinstance(s, Adam8State) for s in states):
@@ -722,17 +728,15 @@ def adamw_mixed_bind(params: Sequence, grads: Sequence, states: Sequence, hyper,
     hp_ref = ctypes.byref(hp)
     dptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
     pointers = (dptr(step_dev), dptr(lr_dev), dptr(grad_scale))
-    args = (arr, n, hp_ref, int(step), *pointers)
+    args = (arr, n, hp_ref, step, *pointers)
     call = _bound(lib().adamw_mixed_batched, "adamw_mixed_batched", dev,
                   (arr, hp, written, read))
 
     def run(step_now: Optional[int] = None, stream=None):
         if step_now is None:
             call(args, stream)
-        elif int(step_now) > 0x7FFFFFFF:
-            raise ValueError(f"step {step_now} does not fit 32 bits")
         else:
-            call((arr, n, hp_ref, int(step_now), *pointers), stream)
+            call((arr, n, hp_ref, _int32(step_now, "step_now"), *pointers), stream)
     return run
 
 
