@@ -598,6 +598,15 @@ class Adam8State:
     def blocks(numel: int) -> int:
         return -(-numel // ADAM8_BLOCK)
 
+    def _checked(self, numel, device, i):
+        """(exp_avg, root, scale) of the state at place i of a call, checked again:
+        a checkpoint's loader may have put others in their places."""
+        import torch
+        u8 = (torch.uint8,)
+        return (_dense(self.exp_avg, u8, numel, "states[{}].exp_avg", device, i),
+                _dense(self.root, u8, numel, "states[{}].root", device, i),
+                _dense(self.scale, u8, 2 * self.blocks(numel), "states[{}].scale", device, i))
+
     @classmethod
     def zeros(cls, numel: int, device=None) -> "Adam8State":
         import torch
@@ -689,14 +698,13 @@ def adamw_mixed_bind(params: Sequence, grads: Sequence, states: Sequence, hyper,
     dev = next((t.device for t in (*params, step_dev) if isinstance(t, torch.Tensor)), None)
     written, read = [], []
     arr = (adamw_mixed_tensor_t * max(n, 1))()
-    b16, either, u8 = (torch.bfloat16,), (torch.float32, torch.bfloat16), (torch.uint8,)
+    b16, either = (torch.bfloat16,), (torch.float32, torch.bfloat16)
     for i in range(n):
         p = _dense(params[i], f32, None, "params[{}]", dev, i)
         k = p.numel()
         g = _dense(grads[i], either, k, "grads[{}]", dev, i)
         if isinstance(states[i], Adam8State):
-            m, v, s = states[i].exp_avg, states[i].root, states[i].scale
-            _dense(m, u8, k, "states[{}].exp_avg", dev, i)
+            m, v, s = states[i]._checked(k, dev, i)
         else:
             (m, v), s = states[i], None
             _dense(m, f32, k, "states[{}][0]", dev, i)
@@ -755,15 +763,15 @@ def _adam8_bind(states, exp_avgs, seconds, write: bool):
     if dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"plain moments must be torch.float32 or torch.bfloat16, got {dtype}")
     dev = states[0].exp_avg.device if n else None
-    coded, plain, u8, kind = [], [], (torch.uint8,), (dtype,)
+    coded, plain, kind = [], [], (dtype,)
     for i, (s, m, v) in enumerate(zip(states, exp_avgs, seconds)):
-        _dense(s.exp_avg, u8, s.numel, "states[{}].exp_avg", dev, i)
+        m8, r8, sc = s._checked(s.numel, dev, i)
         _dense(m, kind, s.numel, "exp_avgs[{}]", dev, i)
         _dense(v, kind, s.numel, "seconds[{}]", dev, i)
-        arr[i] = adam8_tensor_t(s.exp_avg.data_ptr(), s.root.data_ptr(), s.scale.data_ptr(),
+        arr[i] = adam8_tensor_t(m8.data_ptr(), r8.data_ptr(), sc.data_ptr(),
                                 m.data_ptr(), v.data_ptr(), s.numel)
-        coded += ((s.exp_avg, "states[{}].exp_avg", i), (s.root, "states[{}].root", i),
-                  (s.scale, "states[{}].scale", i))
+        coded += ((m8, "states[{}].exp_avg", i), (r8, "states[{}].root", i),
+                  (sc, "states[{}].scale", i))
         plain += ((m, "exp_avgs[{}]", i), (v, "seconds[{}]", i))
     _check_overlap(coded if write else plain, plain if write else coded)
     what = "adam8_write_batched" if write else "adam8_read_batched"
