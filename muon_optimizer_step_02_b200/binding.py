@@ -776,8 +776,7 @@ def _adam8_bind(states, exp_avgs, seconds, write: bool):
     _check_overlap(coded if write else plain, plain if write else coded)
     what = "adam8_write_batched" if write else "adam8_read_batched"
     args = (arr, n, MUON_BF16 if dtype == torch.bfloat16 else MUON_F32)
-    call = _bound(getattr(lib(), what), what, dev,
-                  (arr, list(states), list(exp_avgs), list(seconds)))
+    call = _bound(getattr(lib(), what), what, dev, (arr, coded, plain))
 
     def run(stream=None):
         call(args, stream)

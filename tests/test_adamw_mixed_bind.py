@@ -96,3 +96,22 @@ def test_states_whose_tensors_are_on_the_host_are_refused(call, key):
     setattr(s, key, torch.zeros(4 if key == "scale" else 300, dtype=torch.uint8))
     with pytest.raises(ValueError, match=f"{key} must be a CUDA tensor"):
         bound(call, s)
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_bound_calls_keep_the_state_tensors_that_they_write(call):
+    """Replacing a state's tensors after a bind leaves the bound ones alive: the
+    call still writes to them."""
+    import gc
+    import weakref
+
+    import torch
+    s = states_with()
+    refs = [weakref.ref(t) for t in (s.exp_avg, s.root, s.scale)]
+    run = bound(call, s)
+    s.exp_avg, s.root, s.scale = (on_device(torch.zeros(n, dtype=torch.uint8)) for n in (300, 300, 4))
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    del run
+    gc.collect()
+    assert all(r() is None for r in refs)
