@@ -346,7 +346,10 @@ typedef struct {
  *   out[0] = sqrt(sum of squares);  out[1] = min(1, max_norm / (out[0] + 1e-6)),
  * squares and sums in 64 bits, each result rounded once to fp32 (a norm past
  * fp32's range is infinite there, its coefficient is not affected).  If a
- * gradient is not finite, out[0] is not finite and out[1] is NaN.
+ * gradient is not finite, out[0] is not finite and out[1] is NaN.  Of this
+ * library's calls only adamw_mixed_batched reads the coefficient: the Muon
+ * step neither scales its gradients by it nor skips on NaN.  The norm is of
+ * the gradients given; nothing is reduced across ranks.
  *  max_norm   > 0; infinite: out[1] is 1 for finite gradients.
  *  workspace  device, grad_norm_workspace_bytes() bytes, 16-byte aligned,
  *             zero before its first use; each call leaves it ready for the

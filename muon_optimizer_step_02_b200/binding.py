@@ -625,7 +625,9 @@ def grad_norm_workspace(device=None):
 def grad_norm_bind(grads: Sequence, max_norm: float, out, workspace):
     """Marshals grad_norm_batched once and returns `run(stream=None)`: the norm
     of all gradients (contiguous fp32 or bf16 CUDA tensors) to out[0] and the
-    coefficient that clips it at max_norm to out[1] (out: two fp32)."""
+    coefficient that clips it at max_norm to out[1] (out: two fp32; NaN if a
+    gradient is not finite).  adamw_mixed_bind reads the coefficient as its
+    grad_scale; the Muon step does not.  Nothing is reduced across ranks."""
     import torch
     n = len(grads)
     dev = _dense(out, (torch.float32,), 2, "out").device
