@@ -253,7 +253,7 @@ typedef enum { MUON_F32 = 0, MUON_BF16 = 1 } muon_dtype_t;
  * 0.999, and raises the mean of its square by up to 0.1 %, 0.7 % and 5 %. */
 typedef enum { MUON_ROUND_NEAREST = 0, MUON_ROUND_STOCHASTIC = 1 } muon_round_t;
 
-/* Settings of adamw_mixed_batched.  lr, weight_decay, ema_decay finite;
+/* Settings of adamw_mixed_batched.  lr, weight_decay, ema_decay finite in fp32;
  * beta1, beta2 in [0, 1); eps 0 or at least 2^-126 (fp32's least normal
  * value).  With eps = 0 an element whose moments are zero becomes NaN, as the
  * formula's 0 / 0.  seed gives the random bits of

@@ -24,6 +24,9 @@ constexpr int kFewSegs = 16;   // launches of few tensors carry a short table
 // which an eps down there would leave of elements without moments.
 constexpr double kLeastEps = 0x1p-126;
 
+// The kernels take settings in fp32.
+inline bool finite32(double x) { return std::isfinite(static_cast<float>(x)); }
+
 inline uintptr_t bits(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 
 inline uint32_t units_of(int64_t numel, int unit) {
@@ -228,8 +231,8 @@ muon_status_t adamw_mixed_batched(const adamw_mixed_tensor_t* tensors, int32_t n
                                   const float* coef_dev, muon_stream_t stream) {
   if (n_tensors < 0 || !hyper || (n_tensors > 0 && !tensors)) return MUON_ERR_INVALID_ARG;
   const adamw_mixed_hyper_t& h = *hyper;
-  if (!std::isfinite(h.lr) || !std::isfinite(h.weight_decay) || !std::isfinite(h.eps) ||
-      !std::isfinite(h.ema_decay) || !(h.beta1 >= 0.0 && h.beta1 < 1.0) ||
+  if (!finite32(h.lr) || !finite32(h.weight_decay) || !std::isfinite(h.eps) ||
+      !finite32(h.ema_decay) || !(h.beta1 >= 0.0 && h.beta1 < 1.0) ||
       !(h.beta2 >= 0.0 && h.beta2 < 1.0))
     return MUON_ERR_INVALID_ARG;
   if (h.eps != 0.0 && !(h.eps >= kLeastEps))
