@@ -22,8 +22,8 @@
 // the measured copy bandwidth), 174-190 us with 8-bit ones, rounded
 // stochastically (16 bytes: 5.6-6.2 TB/s, 0.86-0.94), 195-200 us when it runs on
 // end, for then the GPU's power limit lowers the clock.  The 8-bit step is
-// bound by memory and by issue about equally (565 instructions per warp and
-// block of 256, an issue slot in use in 7 of 10 cycles), so it is built to
+// bound by memory and by issue about equally (573 instructions per warp and
+// block of 256, an issue slot in use in 77 of 100 cycles), so it is built to
 // issue little: two elements to a register pair wherever the arithmetic has a
 // two-value form, addresses and tensor look-up in uniform registers, the next
 // block's data on their way through shared memory while one is computed.
@@ -43,7 +43,7 @@
 namespace muonb200 {
 
 constexpr int kMixThreads = 128;      // 4 warps: a unit of 4 blocks of 256 elements
-constexpr int kMixResident = 6;       // thread blocks per SM (76 registers); 8-bit table above with
+constexpr int kMixResident = 6;       // thread blocks per SM (78 registers); 8-bit table above with
                                       // 5, 6, 7: 179, 174, 194 us
 constexpr int kMixUnit = kMixThreads * 8;
 constexpr int kMixMaxSegs = 400;      // 400 x 76 bytes of kernel parameters (limit 32,764)
@@ -745,7 +745,7 @@ adamw_mixed_kernel(const __grid_constant__ MixParams<kSegs> a) {
 // ---- 8-bit states from and to plain arrays --------------------------------
 
 constexpr int kA8MaxSegs = 500;   // 500 x 52 bytes of kernel parameters
-// Thread blocks per SM, as many as their 36 and 32 registers leave room for
+// Thread blocks per SM, as many as their 37 and 32 registers leave room for
 // (writing with 16: a second, partial round, 10 % slower).
 constexpr int kA8WriteResident = 12, kA8ReadResident = 16;
 
@@ -765,7 +765,8 @@ struct A8Params {
 };
 
 // Plain moments -> codes (rounded to the nearest).  10 bytes per element from
-// fp32: 67 M elements in 104-112 us (6.0-6.4 TB/s).
+// fp32: 67 M elements in 104-112 us (6.0-6.4 TB/s); 6 from bf16: 98 us (4.1 TB/s),
+// the ALU pipe in use in 76 of 100 cycles.
 template <int kSegs>
 __global__ void __launch_bounds__(kMixThreads)
 adam8_write_kernel(const __grid_constant__ A8Params<kSegs> a) {
@@ -854,7 +855,7 @@ struct A8Codes {
 // (first moment, second moment = root squared, exact too: 12 bits).  6 bytes per
 // element to bf16.  The next block's codes are requested before this one's are
 // used: the 11L model's 212 tensors 8.1 -> 7.1 us, at the price of 67 -> 71 us
-// (5.7 TB/s) on 67 M elements.
+// (5.7 TB/s) on 67 M elements; 10 bytes per element to fp32: 118 us (5.7 TB/s).
 template <int kSegs>
 __global__ void __launch_bounds__(kMixThreads, kA8ReadResident)
 adam8_read_kernel(const __grid_constant__ A8Params<kSegs> a) {

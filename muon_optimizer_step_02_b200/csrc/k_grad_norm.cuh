@@ -11,10 +11,13 @@
 // every run.  Tensors past one launch's table go into further launches, each
 // adding its sum to the workspace's carry.
 //
-// Bound by memory: 4 or 2 bytes per element.  Each thread block keeps four
-// chunks of 2,048 elements in flight (two: 77 us, eight: 60 us on the first
-// figure below; small gradients come in more even shares with fewer).  The
-// conversions to 64 bits fill 60 % of their pipe at that rate and the GPU's
+// Bound by memory: 4 or 2 bytes per element.  A thread block's loads are
+// written four chunks of 2,048 elements ahead of their use (two: 77 us, eight:
+// 60 us on the first figure below; small gradients come in more even shares
+// with fewer).  For bf16 those are 16 registers of data, all in flight at once;
+// for fp32 they would be 32, as many as a thread has here, so not all can
+// be, and 8 bytes are spilled (4 thread blocks per SM, 64 registers: none).  The
+// conversions to 64 bits fill 71 % of their pipe at that rate and the GPU's
 // power limit lowers the clock when the call runs on end.  184 M bf16
 // gradients: 60 us (6.1 TB/s, 0.94 of the measured copy bandwidth), 69 us on
 // end; 67 M fp32: 43 us (6.2 TB/s).
@@ -32,9 +35,9 @@ namespace muonb200 {
 
 constexpr int kNormThreads = 256;
 constexpr int kNormChunk = kNormThreads * 8;
-constexpr int kNormDeep = 4;          // chunks of a unit, all requested at once
+constexpr int kNormDeep = 4;          // chunks of a unit
 constexpr int kNormUnit = kNormDeep * kNormChunk;
-constexpr int kNormResident = 8;      // thread blocks per SM (32 registers)
+constexpr int kNormResident = 8;      // thread blocks per SM (32 registers, 8 bytes spilled)
 constexpr int kNormMaxSegs = 1300;    // 1300 x 20 bytes of kernel parameters
 constexpr int kNormMaxGrid = 2048;
 
@@ -83,8 +86,8 @@ __device__ __forceinline__ void add_squares(const float2 (&g)[4], double (&sum)[
   }
 }
 
-// kCount whole chunks of a gradient from element i0 on, requested
-// before the first is used.
+// kCount whole chunks of a gradient from element i0 on, requested before the
+// first is used as far as registers allow.
 template <int kCount, bool kG16>
 __device__ __forceinline__ void add_chunks(const void* g, long long i0, double (&sum)[4]) {
   float2 x[4];
