@@ -1,4 +1,4 @@
-"""A step with a bad matrix gradient as the README has it: the norm of all
+"""A step with a bad matrix gradient, withheld as a whole: the norm of all
 gradients first, and the other calls only if its coefficient is a number."""
 import math
 
